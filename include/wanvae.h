@@ -65,7 +65,11 @@ typedef enum {
                                    should not be reused */
 } wanvae_status;
 
-typedef enum { WANVAE_BF16 = 0, WANVAE_F32 = 1 } wanvae_dtype;
+typedef enum {
+    WANVAE_BF16 = 0,
+    WANVAE_F32 = 1,
+    WANVAE_E4M3 = 2 /* a key-value cache's elements only */
+} wanvae_dtype;
 
 /* The CUDA stream type, declared without including the CUDA headers
  * (identical to cudaStream_t). */
@@ -214,6 +218,118 @@ wanvae_status wanvae_frame_attention(const void *x, const float *gamma, const vo
                                      const float *bqkv, const void *wo, const float *bo, void *y,
                                      wanvae_dims d, int64_t c, float eps, void *workspace,
                                      size_t ws_bytes, wanvae_stream stream);
+
+/* Attention over packed sequences of different lengths, causal or full, with
+ * query heads in groups that share a kv head:
+ *   out[i] = sum_j p_ij v[j] / sum_j p_ij,  p_ij = exp(scale q[i] . k[j])
+ * over the keys j of query i's sequence.  Sequence s holds the queries
+ * cu_q[s] .. cu_q[s+1] - 1 and the keys cu_k[s] .. cu_k[s+1] - 1.  Causal: with
+ * Lq queries and Lk keys, query i (from 0) sees the keys j <= i + Lk - Lq, so
+ * that a pass over new tokens alone (Lk > Lq) continues a longer sequence.  A
+ * query that sees no key gives zeros, and what a query does not see does not
+ * reach it, infinities and NaN included.
+ *   q       : bf16 [total_q][n_heads][head_dim], tokens q_stride elements apart
+ *   k, v    : bf16 [total_k][n_kv_heads][head_dim], k_stride / v_stride apart
+ *   out     : bf16, as q, tokens out_stride apart; tokens behind the last
+ *             sequence are left as they were
+ *   cu_q, cu_k : device int32 [n_seq + 1], from 0, not decreasing, at most
+ *             total_q / total_k (a sequence with offsets outside is skipped
+ *             and reported by wanvae_sync_status as WANVAE_ERR_CUDA)
+ *   n_heads : a multiple of n_kv_heads, at most 128 times as many; head h
+ *             reads kv head h / (n_heads / n_kv_heads)
+ *   head_dim : 64 or 128.  Strides: multiples of 8, at least a token's width.
+ * Scores and sums in fp32; the weights are rounded to bf16 for the product.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
+wanvae_status wanvae_packed_attention(const void *q, int64_t q_stride, const void *k,
+                                      int64_t k_stride, const void *v, int64_t v_stride, void *out,
+                                      int64_t out_stride, const int32_t *cu_q,
+                                      const int32_t *cu_k, int64_t n_seq, int64_t total_q,
+                                      int64_t total_k, int64_t n_heads, int64_t n_kv_heads,
+                                      int64_t head_dim, float scale, int causal,
+                                      wanvae_stream stream);
+
+/* A paged key-value cache (all device pointers, caller-owned).  Page j of
+ * sequence s is page_table[s][j] (int32 [n_seq][max_pages], device); position p
+ * of the sequence lies in slot p % page_size of its page p / page_size.
+ *   k, v  : [n_pages][n_kv_heads][page_size][head_dim], of type dt
+ *   dt    : WANVAE_BF16, or WANVAE_E4M3: a row (one token, one head) holds
+ *           e4m3 elements q and one E8M0 scale, x[d] = q[d] * 2^(code - 127)
+ *   k_exp, v_exp : [n_pages][n_kv_heads][page_size] scale codes (E4M3 only)
+ *   page_size : 16, 32, 64, .. 1024.  head_dim : 64 or 128. */
+typedef struct {
+    void *k, *v;
+    uint8_t *k_exp, *v_exp;
+    int64_t n_pages, page_size, n_kv_heads, head_dim;
+    wanvae_dtype dt;
+} wanvae_kv_cache;
+
+/* New rows into the cache, quantised as they are written (dt E4M3): the scale
+ * is the smallest power of two, from 2^-100 to 2^120, that brings the row's
+ * largest magnitude to 448 or below; elements round to nearest, ties to even;
+ * infinities and NaN become NaN and do not count for the scale; a row of zeros
+ * has scale 1.
+ *   k, v   : bf16 [total][n_kv_heads][head_dim], tokens k_stride / v_stride apart
+ *   lens   : device int32 [n_seq], each sequence's length WITH its new tokens
+ *   cu_new : device int32 [n_seq + 1]: sequence s's new tokens are rows
+ *            cu_new[s] .. cu_new[s+1] - 1, its last positions; NULL: one new
+ *            token for each sequence (total = n_seq)
+ * A token whose position or page lies outside the page table or the cache is
+ * not written, and wanvae_sync_status reports WANVAE_ERR_CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
+wanvae_status wanvae_kv_cache_append(const wanvae_kv_cache *cache, const void *k,
+                                     int64_t k_stride, const void *v, int64_t v_stride,
+                                     const int32_t *lens, const int32_t *page_table,
+                                     int64_t max_pages, const int32_t *cu_new, int64_t n_seq,
+                                     int64_t total, wanvae_stream stream);
+
+/* The cache read back, packed, for wanvae_packed_attention over new tokens:
+ * positions 0 .. of sequence s to the rows cu[s] .. cu[s+1] - 1 of k and v
+ * (bf16 [total][n_kv_heads][head_dim], tokens k_stride / v_stride apart).  Rows
+ * behind the last sequence, and rows whose page lies outside the page table
+ * or the cache (reported as for wanvae_kv_cache_append), are left as they were.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
+wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t *page_table,
+                                     int64_t max_pages, const int32_t *cu, int64_t n_seq,
+                                     int64_t total, void *k, int64_t k_stride, void *v,
+                                     int64_t v_stride, wanvae_stream stream);
+
+/* Attention of one new token for each sequence over the cache:
+ *   out[b] = softmax(scale q[b] k^T) v over the first lens[b] cached positions
+ * of sequence b (its new token is appended first); zeros where lens[b] = 0.
+ *   q, out : bf16 [n_seq][n_heads][head_dim], tokens q_stride / out_stride apart
+ *   lens   : device int32 [n_seq], at most max_pages * page_size each.  Lengths
+ *            and pages outside their range are left out and reported by
+ *            wanvae_sync_status as WANVAE_ERR_CUDA.
+ *   workspace : wanvae_paged_attention_workspace_size() bytes, 256-byte aligned,
+ *            contents ignored; not shared by calls that overlap on the GPU.
+ * The cache's rows are split over the whole GPU by their number, so the result
+ * of a sequence depends on the other sequences' lengths in its last bits.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA. */
+size_t wanvae_paged_attention_workspace_size(int64_t n_heads, int64_t n_kv_heads,
+                                             int64_t head_dim);
+wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
+                                     const wanvae_kv_cache *cache, const int32_t *lens,
+                                     const int32_t *page_table, int64_t max_pages, int64_t n_seq,
+                                     int64_t n_heads, float scale, void *out, int64_t out_stride,
+                                     void *workspace, size_t ws_bytes, wanvae_stream stream);
+
+/* The norms after and before a block fused with its gate, residual scale and
+ * residual add, over n_tokens tokens of C channels:
+ *   y = x + residual_scale * gate (.) RMS_norm(f; gamma_post)
+ *   n = RMS_norm(y; gamma_pre)
+ * with RMS_norm as in the ResidualBlock (no SiLU), f the block's output.
+ *   x, f, y, n : [n_tokens][C] of type dt (bf16 or fp32)
+ *   gamma_post : fp32 [C], or NULL: f enters as it is
+ *   gate       : fp32 [ceil(n_tokens / tokens_per_gate)][C], or NULL (one);
+ *                token i has row i / tokens_per_gate (a frame's gate, say)
+ *   gamma_pre  : fp32 [C], or NULL together with n: y alone is written
+ *   Math in fp32, n from y before it is rounded; bf16 rounds to nearest-even.
+ * Errors: INVALID_ARG (as wanvae_rmsnorm_silu), MISALIGNED, CUDA. */
+wanvae_status wanvae_gated_residual_norm(const void *x, const void *f, const float *gamma_post,
+                                         const float *gate, int64_t tokens_per_gate,
+                                         const float *gamma_pre, void *y, void *n,
+                                         wanvae_dtype dt, int64_t n_tokens, int64_t C,
+                                         float residual_scale, float eps, wanvae_stream stream);
 
 /* Bytes of device workspace wanvae_resblock_forward needs for these sizes
  * (the bf16 conv inputs a1 and a2, 256-byte aligned).  0 on invalid sizes. */

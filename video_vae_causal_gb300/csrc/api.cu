@@ -88,6 +88,13 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
+namespace wanvae {
+bool make_launch_ctx(LaunchCtx &ctx, void *stream) {
+    return make_ctx(ctx, static_cast<wanvae_stream>(stream)) == WANVAE_OK;
+}
+void count_launches(int n) { g_launches += (uint64_t)n; }
+}  // namespace wanvae
+
 extern "C" {
 
 const char *wanvae_status_string(wanvae_status s) {

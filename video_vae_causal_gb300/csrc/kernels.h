@@ -20,6 +20,11 @@ struct LaunchCtx {
     int num_sms;
 };
 
+// api.cu: the context of a launch on `stream` of the current device (false: a
+// CUDA call failed), and the count of launches that wanvae_launch_count reports.
+bool make_launch_ctx(LaunchCtx &ctx, void *stream);
+void count_launches(int n);
+
 // Launch `kern` on ctx.stream with programmatic dependent launch allowed (the
 // kernel must call griddep_wait before reading what earlier work wrote).
 template <typename... KArgs, typename... Args>

@@ -1,0 +1,254 @@
+// kv_cache.cu -- the paged key-value cache: rows quantised as they are
+// written, and read back.
+//
+// A cache row is the key (or value) of one token and one kv head, D elements.
+// In 8 bits it is stored as x[d] = 2^e q[d], q e4m3 and e one byte (E8M0) for
+// the row: e is the smallest exponent that brings the row's largest
+// magnitude to 448 (e4m3's largest value) or below, so nothing saturates,
+// dividing by the scale is exact, and a row rounds once, by at most half a
+// step of e4m3 (2^-4 relative, above e4m3's subnormals).  e stays in
+// [-100, 120]: 2^120 * 448 covers every finite bf16 value, and rows below 2^-100
+// round on the grid of 2^-100 (so that attention can carry scales as
+// exponents without leaving fp32's range).  Infinities and NaN become e4m3's
+// NaN and do not count for the scale.
+//
+// Rows lie [page][head][slot][D]: the rows of one head and page are
+// contiguous, which is how attention over the cache reads them.  Both passes
+// move each row once (2 D bytes on one side, D + 1 on the other) and are bound
+// by HBM.  A row takes D / 8 lanes with one 16-byte vector of bf16 each; a
+// warp keeps the rows of a token's heads together, so that the token's
+// sequence and page are looked up once for all of them.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "norm_act.cuh"
+#include "ptx.cuh"
+#include "seq_dev.cuh"
+#include "seq_ops.h"
+
+namespace wanvae {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kExpMin = -100, kExpMax = 120;
+
+struct CacheArgs {
+    uint8_t *k, *v;
+    uint8_t *k_exp, *v_exp;
+    int n_pages, log2_page, H;
+    const int32_t *table;
+    int max_pages;
+    unsigned *err;
+};
+
+// Where a token lies in the cache: the row of head 0 (rows of later heads
+// follow a page's height apart); -1 where the page table has no such page.
+__device__ __forceinline__ int64_t cache_row(const CacheArgs &c, int seq, int pos) {
+    const int page_no = pos >> c.log2_page;
+    int page = -1;
+    if (pos >= 0 && page_no < c.max_pages) page = __ldg(c.table + (int64_t)seq * c.max_pages + page_no);
+    if ((unsigned)page >= (unsigned)c.n_pages) return -1;
+    return (((int64_t)page * c.H) << c.log2_page) + (pos & ((1 << c.log2_page) - 1));
+}
+
+// The scale's exponent of a row whose largest finite magnitude is amax:
+// ceil(log2(amax / 448)), from amax's own bits (448 = 1.75 * 2^8).
+__device__ __forceinline__ int row_exponent(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    if (b == 0u) return 0;
+    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, kExpMin), kExpMax);
+}
+
+// 8 bf16 values -> e4m3 with the row's scale; kLanes lanes hold the row.
+template <int kLanes>
+__device__ __forceinline__ uint2 quantise8(const uint4 &v, int &e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[8];
+    uint32_t amax = 0;  // magnitudes compare as integers; only finite ones count
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = nact_lo(w[i]);
+        x[2 * i + 1] = nact_hi(w[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t m = __float_as_uint(x[i]) & 0x7fffffffu;
+        const bool finite = m < 0x7f800000u;
+        amax = max(amax, finite ? m : 0u);
+        x[i] = finite ? x[i] : __uint_as_float(0x7fc00000u);
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1)
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    e = row_exponent(__uint_as_float(amax));
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = f32x2_to_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+
+// 8 e4m3 values of a row -> bf16 (exact for scales that leave bf16's range alone).
+__device__ __forceinline__ uint4 dequantise8(const uint2 &q, uint32_t code) {
+    const float s = e8m0_value(code);
+    const uint32_t w[2] = {q.x, q.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t h = e4m3x2_to_f16x2(w[i >> 1] >> (16 * (i & 1)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        o[i] = nact_pack(f.x * s, f.y * s);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Rows cu_new[s] .. of k and v to the last positions of sequence s.
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(kThreads)
+kv_append_kernel(const CacheArgs c, const __nv_bfloat16 *__restrict__ k, int64_t k_stride,
+                 const __nv_bfloat16 *__restrict__ v, int64_t v_stride,
+                 const int32_t *__restrict__ lens, const int32_t *__restrict__ cu_new, int n_seq,
+                 int total) {
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a warp holds
+    const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
+    const int warps = (gridDim.x * kThreads) >> 5;
+    for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < total; t += warps) {
+        int seq = t, first = t, end = t + 1;
+        if (cu_new) {
+            seq = seq_of_row(cu_new, n_seq, t);
+            first = __ldg(cu_new + seq);
+            end = __ldg(cu_new + seq + 1);
+        }
+        if (t < first || t >= end) continue;  // a row behind the last sequence
+        const int64_t row0 = cache_row(c, seq, __ldg(lens + seq) - (end - t));
+        if (row0 < 0) {
+            if (lane == 0) atomicOr(c.err, kDevErrAlign);
+            continue;
+        }
+        // the token's H key rows, then its H value rows
+        for (int r0 = 0; r0 < 2 * c.H; r0 += kRows) {
+            const int r = r0 + grp;
+            const bool there = r < 2 * c.H, is_v = r >= c.H;
+            const int h = is_v ? r - c.H : r;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (there)
+                x = __ldg(reinterpret_cast<const uint4 *>((is_v ? v + t * v_stride
+                                                                : k + t * k_stride) +
+                                                          h * D) + sub);
+            const int64_t row = row0 + ((int64_t)h << c.log2_page);
+            uint8_t *dst = (is_v ? c.v : c.k) + row * (kQuant ? D : 2 * D);
+            if (kQuant) {
+                int e;
+                const uint2 q = quantise8<kLanes>(x, e);
+                if (!there) continue;
+                reinterpret_cast<uint2 *>(dst)[sub] = q;
+                if (sub == 0) (is_v ? c.v_exp : c.k_exp)[row] = (uint8_t)(e + 127);
+            } else if (there) {
+                reinterpret_cast<uint4 *>(dst)[sub] = x;
+            }
+        }
+    }
+}
+
+// Positions 0 .. of sequence s to rows cu[s] .. of k and v.
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(kThreads)
+kv_gather_kernel(const CacheArgs c, const int32_t *__restrict__ cu, int n_seq, int total,
+                 __nv_bfloat16 *__restrict__ k, int64_t k_stride, __nv_bfloat16 *__restrict__ v,
+                 int64_t v_stride) {
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
+    const int warps = (gridDim.x * kThreads) >> 5;
+    for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < total; t += warps) {
+        const int seq = seq_of_row(cu, n_seq, t);
+        const int first = __ldg(cu + seq);
+        if (t < first || t >= __ldg(cu + seq + 1)) continue;
+        const int64_t row0 = cache_row(c, seq, t - first);
+        if (row0 < 0) {
+            if (lane == 0) atomicOr(c.err, kDevErrAlign);
+            continue;
+        }
+        for (int r0 = 0; r0 < 2 * c.H; r0 += kRows) {
+            const int r = r0 + grp;
+            if (r >= 2 * c.H) continue;
+            const bool is_v = r >= c.H;
+            const int h = is_v ? r - c.H : r;
+            const int64_t row = row0 + ((int64_t)h << c.log2_page);
+            const uint8_t *src = (is_v ? c.v : c.k) + row * (kQuant ? D : 2 * D);
+            uint4 x;
+            if (kQuant)
+                x = dequantise8(__ldg(reinterpret_cast<const uint2 *>(src) + sub),
+                                __ldg((is_v ? c.v_exp : c.k_exp) + row));
+            else
+                x = __ldg(reinterpret_cast<const uint4 *>(src) + sub);
+            reinterpret_cast<uint4 *>((is_v ? v + t * v_stride : k + t * k_stride) + h * D)[sub] =
+                x;
+        }
+    }
+}
+
+CacheArgs cache_args(const KvCacheSpec &c, const int32_t *table, int max_pages,
+                     const LaunchCtx &ctx) {
+    CacheArgs a;
+    a.k = static_cast<uint8_t *>(c.k);
+    a.v = static_cast<uint8_t *>(c.v);
+    a.k_exp = c.k_exp;
+    a.v_exp = c.v_exp;
+    a.n_pages = c.n_pages;
+    a.log2_page = c.log2_page;
+    a.H = c.H;
+    a.table = table;
+    a.max_pages = max_pages;
+    a.err = ctx.err;
+    return a;
+}
+
+// One token a warp, at most 8 resident blocks a multiprocessor.
+unsigned grid_of(int total, const LaunchCtx &ctx) {
+    return (unsigned)std::min((total + kThreads / 32 - 1) / (kThreads / 32), ctx.num_sms * 8);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvCacheSpec &c, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, const int32_t *lens, const int32_t *table,
+                             int max_pages, const int32_t *cu_new, int n_seq, int total,
+                             const LaunchCtx &ctx) {
+    const CacheArgs a = cache_args(c, table, max_pages, ctx);
+    auto *kp = static_cast<const __nv_bfloat16 *>(k);
+    auto *vp = static_cast<const __nv_bfloat16 *>(v);
+    const dim3 grid(grid_of(total, ctx)), block(kThreads);
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, grid, block, 0, ctx, a, kp, k_stride, vp, v_stride, lens, cu_new,
+                          n_seq, total);
+    };
+    if (c.D == 64) return c.e4m3 ? go(kv_append_kernel<64, true>) : go(kv_append_kernel<64, false>);
+    if (c.D == 128)
+        return c.e4m3 ? go(kv_append_kernel<128, true>) : go(kv_append_kernel<128, false>);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_kv_gather(const KvCacheSpec &c, const int32_t *table, int max_pages,
+                             const int32_t *cu, int n_seq, int total, void *k, int64_t k_stride,
+                             void *v, int64_t v_stride, const LaunchCtx &ctx) {
+    const CacheArgs a = cache_args(c, table, max_pages, ctx);
+    auto *kp = static_cast<__nv_bfloat16 *>(k);
+    auto *vp = static_cast<__nv_bfloat16 *>(v);
+    const dim3 grid(grid_of(total, ctx)), block(kThreads);
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, grid, block, 0, ctx, a, cu, n_seq, total, kp, k_stride, vp,
+                          v_stride);
+    };
+    if (c.D == 64) return c.e4m3 ? go(kv_gather_kernel<64, true>) : go(kv_gather_kernel<64, false>);
+    if (c.D == 128)
+        return c.e4m3 ? go(kv_gather_kernel<128, true>) : go(kv_gather_kernel<128, false>);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace wanvae

@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libwanvae.so")
 
 (OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT,
  ERR_UNDRAINED) = range(8)
-BF16, F32 = 0, 1
+BF16, F32, E4M3 = 0, 1, 2
 
 # Every exported symbol of include/wanvae.h.
 EXPORTS = (
@@ -27,6 +27,9 @@ EXPORTS = (
     "wanvae_time_upsample_conv", "wanvae_upsample3d_workspace_size", "wanvae_upsample3d",
     "wanvae_frame_attention_workspace_size", "wanvae_frame_attention",
     "wanvae_resblock_forward_host_workspace_size", "wanvae_resblock_forward_host",
+    "wanvae_packed_attention", "wanvae_kv_cache_append", "wanvae_kv_cache_gather",
+    "wanvae_paged_attention_workspace_size", "wanvae_paged_attention",
+    "wanvae_gated_residual_norm",
 )
 
 # Size of the library's own workspace used by resblock_forward_static.
@@ -56,6 +59,14 @@ class ResblockParams(ctypes.Structure):
 
 class ResblockCache(ctypes.Structure):
     _fields_ = [("convA_in", ctypes.c_void_p), ("convB_in", ctypes.c_void_p)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("dt", ctypes.c_int)]
 
 
 _lib = None
@@ -122,6 +133,22 @@ def load(path=LIB_PATH):
     L.wanvae_frame_attention.argtypes = [vp, vp, vp, vp, vp, vp, vp, Dims, i64, ctypes.c_float, vp,
                                          ctypes.c_size_t, vp]
     L.wanvae_frame_attention.restype = st
+    cache, f32 = ctypes.POINTER(KvCacheDesc), ctypes.c_float
+    L.wanvae_packed_attention.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, i64,
+                                          i64, i64, i64, i64, f32, ci, vp]
+    L.wanvae_packed_attention.restype = st
+    L.wanvae_kv_cache_append.argtypes = [cache, vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, vp]
+    L.wanvae_kv_cache_append.restype = st
+    L.wanvae_kv_cache_gather.argtypes = [cache, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp]
+    L.wanvae_kv_cache_gather.restype = st
+    L.wanvae_paged_attention_workspace_size.argtypes = [i64, i64, i64]
+    L.wanvae_paged_attention_workspace_size.restype = ctypes.c_size_t
+    L.wanvae_paged_attention.argtypes = [vp, i64, cache, vp, vp, i64, i64, i64, f32, vp, i64, vp,
+                                         ctypes.c_size_t, vp]
+    L.wanvae_paged_attention.restype = st
+    L.wanvae_gated_residual_norm.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, ci, i64, i64, f32,
+                                             f32, vp]
+    L.wanvae_gated_residual_norm.restype = st
     _lib = L
     return L
 
@@ -361,3 +388,227 @@ def resblock_forward_static(x, params, y, cache=None, stream=None):
     _check(st, "wanvae_resblock_forward_static")
     del keep_alive
     return y
+
+
+# ------------------------------------------------------------------ sequences
+def _fit(where, ok):
+    """Refuse a call whose tensors do not fit it."""
+    if not ok:
+        raise WanvaeError(ERR_INVALID_ARG, where)
+
+
+def _on_device(where, *tensors):
+    """Every tensor (None: absent) lies on the current device: its context is
+    the one that the library launches in."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise WanvaeError(ERR_INVALID_ARG, where)
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise WanvaeError(ERR_INVALID_ARG, where)
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _heads(where, t, dtype=torch.bfloat16):
+    """Token stride of [tokens, heads, D] whose tokens are each contiguous."""
+    _fit(where, t.dim() == 3 and t.dtype == dtype)
+    n, h, d = t.shape
+    _fit(where, (h == 1 or t.stride(1) == d) and (d == 1 or t.stride(2) == 1))
+    return t.stride(0) if n > 1 else max(t.stride(0), h * d)
+
+
+def _ints(where, t, *shape):
+    _fit(where, t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape)
+
+
+def _ours(t, stream):
+    """A tensor allocated here for work on a stream that may not be current."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def packed_attention(q, k, v, cu_q, cu_k=None, out=None, causal=True, scale=None, stream=None):
+    """Attention over packed sequences of different lengths.  q [Tq, Hq, D], k
+    and v [Tk, Hkv, D] bf16 (tokens may be strided, as slices of one projection
+    are), cu_q and cu_k int32 [n + 1] offsets on the device (cu_k: cu_q unless
+    given); causal: the last query of a sequence sees all of its keys.  Rows of
+    `out` behind the last sequence are left as they were."""
+    where = "wanvae_packed_attention"
+    if cu_k is None:
+        cu_k = cu_q
+    n = cu_q.numel() - 1
+    if out is None:
+        out = _ours(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
+    _on_device(where, q, k, v, cu_q, cu_k, out)
+    _ints(where, cu_q, n + 1)
+    _ints(where, cu_k, n + 1)
+    qs, ks, vs, os_ = _heads(where, q), _heads(where, k), _heads(where, v), _heads(where, out)
+    _fit(where, out.shape == q.shape and k.shape == v.shape and q.shape[2] == k.shape[2])
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    st = load().wanvae_packed_attention(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, out.data_ptr(), os_,
+        cu_q.data_ptr(), cu_k.data_ptr(), n, Tq, Tk, Hq, Hkv, D,
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, _raw_stream(stream))
+    _check(st, where)
+    return out
+
+
+class KVCache:
+    """A paged key-value cache over the caller's tensors: k and v
+    [n_pages, Hkv, page_size, D], bf16, or float8_e4m3fn with k_exp and v_exp
+    [n_pages, Hkv, page_size] (float8_e8m0fnu or uint8), one scale a row."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        where = "wanvae_kv_cache"
+        _fit(where, k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and
+             k.is_contiguous() and v.is_contiguous())
+        _fit(where, k.dtype in (torch.bfloat16, torch.float8_e4m3fn))
+        quant = k.dtype == torch.float8_e4m3fn
+        for e in (k_exp, v_exp):
+            _fit(where, (e is not None) == quant)
+            _fit(where, e is None or (e.element_size() == 1 and e.is_contiguous() and
+                                      e.shape == k.shape[:3]))
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        n, self.heads, self.page_size, self.head_dim = k.shape
+        self.desc = KvCacheDesc(_raw(k), _raw(v), _raw(k_exp), _raw(v_exp), n, self.page_size,
+                                self.heads, self.head_dim, E4M3 if quant else BF16)
+        self.ref = ctypes.byref(self.desc)
+
+    def tensors(self):
+        return self.k, self.v, self.k_exp, self.v_exp
+
+
+def make_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4m3fn,
+                  device="cuda"):
+    """An empty paged cache, in 8 bits (float8_e4m3fn) or bf16."""
+    shape = (n_pages, n_kv_heads, page_size, head_dim)
+    k, v = (torch.zeros(shape, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype,
+                        device=device).view(dtype) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return KVCache(k, v)
+    ke, ve = (torch.full(shape[:3], 127, dtype=torch.uint8, device=device)
+              .view(torch.float8_e8m0fnu) for _ in range(2))
+    return KVCache(k, v, ke, ve)
+
+
+def kv_cache_append(cache, k, v, lens, page_table, cu_new=None, stream=None):
+    """New rows k, v [T, Hkv, D] bf16 into the cache: the last positions of
+    sequences whose lengths with them are lens (int32 [n], device).  cu_new
+    int32 [n + 1]: sequence s has rows cu_new[s] .. cu_new[s + 1] - 1; None: one
+    row a sequence.  page_table int32 [n, max_pages]."""
+    where = "wanvae_kv_cache_append"
+    _on_device(where, k, v, lens, page_table, cu_new, *cache.tensors())
+    ks, vs = _heads(where, k), _heads(where, v)
+    _fit(where, k.shape == v.shape and k.shape[1:] == (cache.heads, cache.head_dim) and
+         page_table.dim() == 2)
+    n, max_pages = page_table.shape
+    _ints(where, lens, n)
+    _ints(where, page_table, n, max_pages)
+    if cu_new is not None:
+        _ints(where, cu_new, n + 1)
+    st = load().wanvae_kv_cache_append(cache.ref, k.data_ptr(), ks, v.data_ptr(), vs,
+                                       lens.data_ptr(), page_table.data_ptr(), max_pages,
+                                       _raw(cu_new), n, k.shape[0], _raw_stream(stream))
+    _check(st, where)
+
+
+def kv_cache_gather(cache, page_table, cu, k=None, v=None, total=None, stream=None):
+    """The cache read back, packed: positions 0 .. of sequence s to the rows
+    cu[s] .. cu[s + 1] - 1 of k and v [total, Hkv, D] bf16 (cu int32 [n + 1],
+    device).  Without k and v, `total` rows are allocated."""
+    where = "wanvae_kv_cache_gather"
+    if k is None or v is None:
+        _fit(where, k is None and v is None and total is not None)
+        k, v = (_ours(torch.empty((total, cache.heads, cache.head_dim), dtype=torch.bfloat16,
+                                  device=page_table.device), stream) for _ in range(2))
+    _on_device(where, k, v, cu, page_table, *cache.tensors())
+    ks, vs = _heads(where, k), _heads(where, v)
+    _fit(where, k.shape == v.shape and k.shape[1:] == (cache.heads, cache.head_dim) and
+         page_table.dim() == 2)
+    n, max_pages = page_table.shape
+    _ints(where, cu, n + 1)
+    _ints(where, page_table, n, max_pages)
+    st = load().wanvae_kv_cache_gather(cache.ref, page_table.data_ptr(), max_pages, cu.data_ptr(),
+                                       n, k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs,
+                                       _raw_stream(stream))
+    _check(st, where)
+    return k, v
+
+
+def paged_attention_workspace_size(n_heads, n_kv_heads, head_dim):
+    return int(load().wanvae_paged_attention_workspace_size(n_heads, n_kv_heads, head_dim))
+
+
+def make_paged_attention_workspace(q, cache):
+    """A workspace for paged_attention of q's heads over the cache."""
+    n = paged_attention_workspace_size(q.shape[1], cache.heads, cache.head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_attention(q, cache, lens, page_table, out=None, workspace=None, scale=None,
+                    stream=None):
+    """Attention of one new token for each sequence, q [n, Hq, D] bf16, over the
+    first lens[s] positions of the cache (lens int32 [n], page_table int32
+    [n, max_pages], device); zeros where lens[s] is 0."""
+    where = "wanvae_paged_attention"
+    if out is None:
+        out = _ours(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
+    if workspace is None:
+        workspace = _ours(make_paged_attention_workspace(q, cache), stream)
+    _on_device(where, q, lens, page_table, out, workspace, *cache.tensors())
+    qs, os_ = _heads(where, q), _heads(where, out)
+    _fit(where, out.shape == q.shape and q.shape[2] == cache.head_dim and page_table.dim() == 2)
+    n, Hq, D = q.shape
+    max_pages = page_table.shape[1]
+    _ints(where, lens, n)
+    _ints(where, page_table, n, max_pages)
+    st = load().wanvae_paged_attention(q.data_ptr(), qs, cache.ref, lens.data_ptr(),
+                                       page_table.data_ptr(), max_pages, n, Hq,
+                                       D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                                       workspace.data_ptr(), workspace.nbytes,
+                                       _raw_stream(stream))
+    _check(st, where)
+    return out
+
+
+def gated_residual_norm(x, f, gamma_post=None, gate=None, gamma_pre=None, tokens_per_gate=1,
+                        residual_scale=1.0, y=None, n=None, eps=1e-12, stream=None):
+    """y = x + residual_scale * gate * RMS_norm(f; gamma_post) and, with
+    gamma_pre, n = RMS_norm(y; gamma_pre), over the last axis of x and f (bf16
+    or fp32, contiguous).  gate fp32 [G, C]: token i has row i // tokens_per_gate.
+    Returns (y, n); n is None without gamma_pre."""
+    where = "wanvae_gated_residual_norm"
+    _fit(where, x.dtype in (torch.bfloat16, torch.float32))
+    if y is None:
+        y = _ours(torch.empty_like(x), stream)
+    if n is None and gamma_pre is not None:
+        n = _ours(torch.empty_like(x), stream)
+    _on_device(where, x, f, gamma_post, gate, gamma_pre, y, n)
+    for t in (x, f, y, n):
+        _fit(where, t is None or (t.shape == x.shape and t.dtype == x.dtype and
+                                  t.is_contiguous()))
+    C = x.shape[-1]
+    tokens = x.numel() // C if C else 0
+    for t in (gamma_post, gamma_pre):
+        _fit(where, t is None or (t.dtype == torch.float32 and t.is_contiguous() and
+                                  t.shape == (C,)))
+    if gate is not None:
+        _fit(where, gate.dtype == torch.float32 and gate.is_contiguous() and gate.dim() == 2 and
+             gate.shape[1] == C and tokens_per_gate >= 1 and
+             gate.shape[0] * tokens_per_gate >= tokens)
+    st = load().wanvae_gated_residual_norm(
+        x.data_ptr(), f.data_ptr(), _raw(gamma_post), _raw(gate), tokens_per_gate,
+        _raw(gamma_pre), y.data_ptr(), _raw(n), BF16 if x.dtype == torch.bfloat16 else F32,
+        tokens, C, residual_scale, eps, _raw_stream(stream))
+    _check(st, where)
+    return y, n
