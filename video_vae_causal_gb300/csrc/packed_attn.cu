@@ -6,17 +6,25 @@
 // over the keys j of query i's own sequence and, where causal, j <= i + Lk - Lq
 // (the last query sees every key).  A query that sees none gives zeros.
 //
-// A CTA owns one kv head and a tile of 128 rows of one sequence: 128 / G
+// A CTA owns one kv head and two tiles of 128 rows of one sequence, each 128 / G
 // consecutive queries times the G query heads of the group, so that short
 // prompts fill the tensor core's rows, keys are read once for the group, and
 // a causal tile's diagonal is G times shorter.  It sweeps the visible keys in
-// blocks of 128:
+// blocks of 128, and for each tile
 //   S = Q K_j^T       (tcgen05, S in TMEM)
-//   P = exp2(S' - m)  (4 softmax warps, one row a thread; P in shared memory)
-//   O += P V_j        (tcgen05, O in TMEM; V as it lies in memory, read along its rows)
-// The running maximum m moves only by more than 2^8, as in the mid-block's
-// core, so P stays <= 256 and O is rarely rescaled.  P rounds to bf16, the type
+//   P = exp2(S' - m)  (a warpgroup of its own, one row a thread; P over S in TMEM)
+//   O += P V_j        (tcgen05, P from TMEM, V as it lies in memory, read along its rows)
+// While one tile's warpgroup computes exponentials the tensor core runs the
+// other tile's products: O += P V_j and the next S of a tile are issued together
+// as soon as its P is there (MMAs of one thread run in order, so the next S may
+// overwrite the P that the product before it reads).  The running maximum m
+// moves only by more than 2^8, as in the mid-block's core, so P stays <= 256 and
+// O is rarely rescaled, by the tile's own warpgroup.  P rounds to bf16, the type
 // that V has (an MMA's operands share one); the sum is of the unrounded P.
+//
+// What bounds it: for D = 128 a block of both tiles is 1024 cycles of MMAs and,
+// per SM quarter, 256 warp instructions of exponentials among about 800; for
+// D = 64 the MMAs halve and the exponentials do not.
 //
 // Masked scores are replaced, never added to, so nothing in a masked key
 // reaches a row.  A masked value's weight is zero, but 0 * NaN is not: the value
@@ -38,10 +46,13 @@
 namespace wanvae {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 384;  // two softmax warpgroups; issuer, producer, two idle warps
+// Registers: 384 threads launch with 168 (64512 in all); the third warpgroup
+// gives back what the softmax warpgroups take: 2 * 128 * 216 + 128 * 72 = 64512.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kRows = 128;                 // rows of a tile, keys of a block
 constexpr uint32_t kAtom = kRows * 128u;   // 128 rows x 64 bf16, 128-byte swizzled
-constexpr int kStages = 2;                 // blocks of K and of V in flight
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 
 struct PackedArgs {
@@ -50,44 +61,52 @@ struct PackedArgs {
     int64_t q_stride, k_stride, v_stride, out_stride;
     const int32_t *cu_q, *cu_k;
     int n_seq, total_q, total_k;
-    int G, nt;         // query heads of a kv head, queries of a tile
+    int Hkv, G, nt;    // kv heads; query heads of one; queries of a tile
     float scale_log2;  // scale * log2(e)
     int causal;
     unsigned *err;
     uint64_t wait_ns;
 };
 
-// A CTA's tile: queries [q0, q0 + nq) of the packed rows; keys [k0, k0 + kend)
-// are seen by one of them or more, query i (in the tile) sees the first
-// min(kend, see + i) of them (see: see0 where causal, kend elsewhere).
+// A CTA's queries [q0, q0 + nq) of the packed rows (tile w holds p.nt of them
+// from q0 + w nt); its sequence's keys [k0, k0 + Lk).  Query i of the CTA sees
+// the first see0 + i keys where causal, else all.
 struct Tile {
-    int q0, nq, k0, kend, see0;
+    int q0, nq, k0, Lk, see0;
 };
 
 template <int D>
 struct Layout {
-    static constexpr uint32_t kTile = (D / 64) * kAtom;  // Q, a block of K, a block of V
-    static constexpr uint32_t kQ = 0, kP = kTile, kK = kP + 2 * kAtom, kV = kK + kStages * kTile;
-    static constexpr uint32_t kBars = kV + kStages * kTile;
+    static constexpr uint32_t kTile = (D / 64) * kAtom;  // a tile of Q, a block of K or V
+    static constexpr int kStages = D == 64 ? 8 : 5;      // blocks of K and V in flight
+    static constexpr uint32_t kQ = 0, kRing = 2 * kTile;
+    static constexpr uint32_t kBars = kRing + kStages * kTile;
     static constexpr uint32_t kSmem = 1024 + kBars + 256;
+    static constexpr uint32_t kO = 256;  // TMEM: S and P of tile w at 128 w, O at 256 + 128 w
 };
 
+// The ring holds K_0, V_0, K_1, V_1, ..
+__device__ __forceinline__ int fill_k(int j) { return 2 * j; }
+__device__ __forceinline__ int fill_v(int j) { return 2 * j + 1; }
+
+template <int D>
 struct Bars {
+    static constexpr int kStages = Layout<D>::kStages;
     uint32_t base;
     __device__ uint32_t q_full() const { return base; }
-    __device__ uint32_t s_full() const { return base + 8; }
-    __device__ uint32_t s_free() const { return base + 16; }
-    __device__ uint32_t p_full() const { return base + 24; }
-    __device__ uint32_t o_done() const { return base + 32; }
-    __device__ uint32_t drain() const { return base + 40; }
-    __device__ uint32_t k_full(int s) const { return base + 48 + 8 * s; }
-    __device__ uint32_t k_empty(int s) const { return base + 48 + 8 * (kStages + s); }
-    __device__ uint32_t v_full(int s) const { return base + 48 + 8 * (2 * kStages + s); }
-    __device__ uint32_t v_empty(int s) const { return base + 48 + 8 * (3 * kStages + s); }
+    __device__ uint32_t drain() const { return base + 8; }
+    __device__ uint32_t s_full(int w) const { return base + 16 + 8 * w; }
+    __device__ uint32_t p_full(int w) const { return base + 32 + 8 * w; }
+    __device__ uint32_t o_full(int w) const { return base + 48 + 8 * w; }
+    __device__ uint32_t full(int fill) const { return base + 64 + 8 * (fill % kStages); }
+    __device__ uint32_t empty(int fill) const {
+        return base + 64 + 8 * (kStages + fill % kStages);
+    }
+    static __device__ uint32_t phase(int fill) { return (uint32_t)(fill / kStages) & 1u; }
 };
 
-// Tile `x` of the launch, counting the tiles of every sequence in order;
-// whole warp.  nq = 0: no such tile.
+// Tile pair `x` of the launch, counting the pairs of every sequence in order;
+// whole warp.  nq = 0: no such pair.
 __device__ Tile find_tile(const PackedArgs &p, int x) {
     const int lane = threadIdx.x & 31;
     Tile r = {0, 0, 0, 0, 0};
@@ -104,7 +123,7 @@ __device__ Tile find_tile(const PackedArgs &p, int x) {
             const bool ok = qa >= 0 && qb >= qa && qb <= p.total_q && ka >= 0 && kb >= ka &&
                             kb <= p.total_k;
             if (!ok && x == 0) atomicOr(p.err, kDevErrAlign);
-            tiles = ok ? (qb - qa + p.nt - 1) / p.nt : 0;
+            tiles = ok ? (qb - qa + 2 * p.nt - 1) / (2 * p.nt) : 0;
         }
         int incl = tiles;
 #pragma unroll
@@ -115,17 +134,18 @@ __device__ Tile find_tile(const PackedArgs &p, int x) {
         const unsigned m = __ballot_sync(0xffffffffu, before + incl > x);
         if (m) {
             const int l = __ffs(m) - 1;
-            const int t = x - before - __shfl_sync(0xffffffffu, incl - tiles, l);
+            // the last queries first: where causal they see the most keys
+            const int t = before + __shfl_sync(0xffffffffu, incl, l) - 1 - x;
             qa = __shfl_sync(0xffffffffu, qa, l);
             qb = __shfl_sync(0xffffffffu, qb, l);
             ka = __shfl_sync(0xffffffffu, ka, l);
             kb = __shfl_sync(0xffffffffu, kb, l);
-            const int Lq = qb - qa, Lk = kb - ka;
-            r.q0 = qa + t * p.nt;
-            r.nq = min(p.nt, Lq - t * p.nt);
+            const int Lq = qb - qa, i0 = t * 2 * p.nt;
+            r.q0 = qa + i0;
+            r.nq = min(2 * p.nt, Lq - i0);
             r.k0 = ka;
-            r.see0 = p.causal ? t * p.nt + Lk - Lq + 1 : Lk;
-            r.kend = p.causal ? min(Lk, max(0, r.see0 + r.nq - 1)) : Lk;
+            r.Lk = kb - ka;
+            r.see0 = i0 + r.Lk - Lq + 1;
             return r;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -165,89 +185,95 @@ __device__ __noinline__ void slow_row(const PackedArgs &p, int q, int head, int 
     for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16(o[e] / l);
 }
 
-// TMA producer (one thread): Q, then K_j and V_j of every block.
+// Keys that a query of tile w sees (0: none, or no such tile).
+__device__ __forceinline__ int keys_of(const PackedArgs &p, const Tile &tl, int w) {
+    const int nq = min(tl.nq - w * p.nt, p.nt);
+    if (nq <= 0) return 0;
+    return p.causal ? min(tl.Lk, max(0, tl.see0 + w * p.nt + nq - 1)) : tl.Lk;
+}
+__device__ __forceinline__ int blocks_of(int keys) { return (keys + kRows - 1) / kRows; }
+
+// TMA producer (one thread): Q, then K_0, V_0, K_1, ..
 template <int D>
 __device__ void producer(const CUtensorMap *mQ, const CUtensorMap *mK, const CUtensorMap *mV,
-                         const PackedArgs &p, const Tile &tl, int kvh, int nkb, uint32_t sbase,
-                         const Bars &bars, const WaitCtl &wc) {
+                         const PackedArgs &p, const Tile &tl, int kvh, int blocks, uint32_t sbase,
+                         const Bars<D> &bars, const WaitCtl &wc) {
     using L = Layout<D>;
-    uint32_t kf = 0, vf = 0;
-    bool ok = true;
-    mbar_arrive_expect_tx(bars.q_full(), (uint32_t)(D / 64) * p.G * p.nt * 128u);
-    for (int a = 0; a < D / 64; ++a)
-        tma_load_3d(sbase + L::kQ + a * kAtom, mQ, bars.q_full(), a * 64, kvh * p.G, tl.q0);
-    for (int j = 0; ok && j < nkb; ++j) {
-        const int s = j % kStages;
-        const uint32_t ph = (uint32_t)(j / kStages) & 1u;
-        ok = mbar_wait<false>(bars.k_empty(s), ph ^ 1u, wc);
-        if (!ok) break;
-        mbar_arrive_expect_tx(bars.k_full(s), L::kTile);
+    const int tiles = tl.nq > p.nt ? 2 : 1;
+    mbar_arrive_expect_tx(bars.q_full(), (uint32_t)(tiles * (D / 64) * p.G * p.nt) * 128u);
+    for (int w = 0; w < tiles; ++w)
         for (int a = 0; a < D / 64; ++a)
-            tma_load_3d(sbase + L::kK + s * L::kTile + a * kAtom, mK, bars.k_full(s), a * 64, kvh,
-                        tl.k0 + j * kRows);
-        ++kf;
-        ok = mbar_wait<false>(bars.v_empty(s), ph ^ 1u, wc);
-        if (!ok) break;
-        mbar_arrive_expect_tx(bars.v_full(s), L::kTile);
+            tma_load_3d(sbase + L::kQ + w * L::kTile + a * kAtom, mQ, bars.q_full(), a * 64,
+                        kvh * p.G, tl.q0 + w * p.nt);
+    int f = 0;
+    for (; f < 2 * blocks; ++f) {
+        if (!mbar_wait<false>(bars.empty(f), bars.phase(f) ^ 1u, wc)) break;
+        mbar_arrive_expect_tx(bars.full(f), L::kTile);
+        const CUtensorMap *m = f & 1 ? mV : mK;
         for (int a = 0; a < D / 64; ++a)
-            tma_load_3d(sbase + L::kV + s * L::kTile + a * kAtom, mV, bars.v_full(s), a * 64, kvh,
-                        tl.k0 + j * kRows);
-        ++vf;
+            tma_load_3d(sbase + L::kRing + (f % L::kStages) * L::kTile + a * kAtom, m, bars.full(f),
+                        a * 64, kvh, tl.k0 + (f >> 1) * kRows);
     }
-    if (!ok) {
+    if (f < 2 * blocks) {
         // Aborted: let every copy in flight land before shared memory goes away.
         volatile int no_abort = 0;
         const WaitCtl dc{kDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
         mbar_wait<false>(bars.q_full(), 0u, dc);
-        for (uint32_t f = kf > kStages ? kf - kStages : 0; f < kf; ++f)
-            mbar_wait<false>(bars.k_full(f % kStages), (f / kStages) & 1u, dc);
-        for (uint32_t f = vf > kStages ? vf - kStages : 0; f < vf; ++f)
-            mbar_wait<false>(bars.v_full(f % kStages), (f / kStages) & 1u, dc);
+        for (int i = f > L::kStages ? f - L::kStages : 0; i < f; ++i)
+            mbar_wait<false>(bars.full(i), bars.phase(i), dc);
     }
 }
 
-// MMA issuer (one thread): S_0, then S_{j+1} and O += P_j V_j for every block.
+// MMA issuer (one thread).  Tile w takes part in blocks j < n[w].
 template <int D>
-__device__ void issuer(int nkb, uint32_t sbase, uint32_t tmem, const Bars &bars,
-                       const WaitCtl &wc) {
+__device__ void issuer(const int (&n)[2], int blocks, uint32_t sbase, uint32_t tmem,
+                       const Bars<D> &bars, const WaitCtl &wc) {
     using L = Layout<D>;
     const uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32_bt(128, D);
     const uint64_t q0 = sdesc_kmajor(sbase + L::kQ, 128u, kLayoutSw128);
-    const uint64_t p0 = sdesc_kmajor(sbase + L::kP, 128u, kLayoutSw128);
-    const uint64_t k0 = sdesc_kmajor(sbase + L::kK, 128u, kLayoutSw128);
-    const uint64_t v0 = sdesc_rows_sw128(sbase + L::kV, kAtom);
-    auto issue_s = [&](int j) -> bool {
-        const int s = j % kStages;
-        if (j > 0 && !mbar_wait<false>(bars.s_free(), (uint32_t)(j - 1) & 1u, wc)) return false;
-        if (!mbar_wait<false>(bars.k_full(s), (uint32_t)(j / kStages) & 1u, wc)) return false;
-        tc_fence_after();
+    const uint64_t k0 = sdesc_kmajor(sbase + L::kRing, 128u, kLayoutSw128);
+    const uint64_t v0 = sdesc_rows_sw128(sbase + L::kRing, kAtom);
+    constexpr uint32_t kTile16 = L::kTile >> 4;
+    auto scores = [&](int w, int j) {  // S = Q K_j^T
+        const uint64_t a = q0 + (uint32_t)w * kTile16;
+        const uint64_t b = k0 + (uint32_t)(fill_k(j) % L::kStages) * kTile16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (uint32_t)(kk >> 2) * (kAtom >> 4) + (kk & 3) * 2;
-            mma_bf16_ss(tmem, q0 + off, k0 + (uint32_t)s * (L::kTile >> 4) + off, id_s, kk > 0);
+            mma_bf16_ss(tmem + 128u * w, a + off, b + off, id_s, kk > 0);
         }
-        mma_commit(bars.k_empty(s));
-        mma_commit(bars.s_full());
-        return true;
+        mma_commit(bars.s_full(w));
     };
-    bool ok = mbar_wait<false>(bars.q_full(), 0u, wc);
-    if (ok) tc_fence_after();
-    ok = ok && issue_s(0);
-    for (int j = 0; ok && j < nkb; ++j) {
-        if (j + 1 < nkb) ok = issue_s(j + 1);
-        const int s = j % kStages;
-        ok = ok && mbar_wait<false>(bars.v_full(s), (uint32_t)(j / kStages) & 1u, wc) &&
-             mbar_wait<false>(bars.p_full(), (uint32_t)j & 1u, wc);
-        if (!ok) break;
+    bool ok = mbar_wait<false>(bars.q_full(), 0u, wc) &&
+              mbar_wait<false>(bars.full(fill_k(0)), 0u, wc);
+    if (ok) {
         tc_fence_after();
+        for (int w = 0; w < 2; ++w)
+            if (n[w] > 0) scores(w, 0);
+        mma_commit(bars.empty(fill_k(0)));
+    }
+    for (int j = 0; ok && j < blocks; ++j) {
+        ok = mbar_wait<false>(bars.full(fill_v(j)), bars.phase(fill_v(j)), wc);
+        if (ok && j + 1 < blocks)
+            ok = mbar_wait<false>(bars.full(fill_k(j + 1)), bars.phase(fill_k(j + 1)), wc);
+        const uint64_t b = v0 + (uint32_t)(fill_v(j) % L::kStages) * kTile16;
+        for (int w = 0; ok && w < 2; ++w) {
+            if (j >= n[w]) continue;
+            ok = mbar_wait<false>(bars.p_full(w), (uint32_t)j & 1u, wc);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk)
-            mma_bf16_ss(tmem + 128u,
-                        p0 + (uint32_t)(kk >> 2) * (kAtom >> 4) + (kk & 3) * 2,
-                        v0 + (uint32_t)s * (L::kTile >> 4) + kk * (2048u >> 4), id_o,
-                        j > 0 || kk > 0);
-        mma_commit(bars.v_empty(s));
-        mma_commit(bars.o_done());
+            for (int kk = 0; kk < kRows / 16; ++kk)
+                mma_bf16_ts(tmem + L::kO + 128u * w, tmem + 128u * w + kk * 8, b + kk * (2048u >> 4),
+                            id_o, j > 0 || kk > 0);
+            if (j + 1 < n[w])
+                scores(w, j + 1);
+            else
+                mma_commit(bars.o_full(w));
+        }
+        if (!ok) break;
+        mma_commit(bars.empty(fill_v(j)));
+        if (j + 1 < blocks) mma_commit(bars.empty(fill_k(j + 1)));
     }
     // Every MMA issued above completes before TMEM is released.
     volatile int no_abort = 0;
@@ -256,87 +282,107 @@ __device__ void issuer(int nkb, uint32_t sbase, uint32_t tmem, const Bars &bars,
     mbar_wait<false>(bars.drain(), 0u, dc);
 }
 
-// Softmax and epilogue (4 warps, one row a thread: the TMEM lane quarter that
-// the warp may access).  Decisions before warp-wide TMEM accesses are uniform.
+// Softmax and epilogue of tile w (4 warps, one row a thread: the TMEM lane
+// quarter that the warp may access).  Decisions before warp-wide TMEM accesses
+// are uniform.  `blocks`: of the CTA.
 template <int D>
-__device__ void softmax(const PackedArgs &p, const Tile &tl, int kvh, int nkb, uint8_t *smem,
-                        uint32_t tmem, const Bars &bars, const WaitCtl &wc) {
+__device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, const int (&n)[2],
+                        int blocks, int keys_cta, uint8_t *smem, uint32_t tmem,
+                        const Bars<D> &bars, const WaitCtl &wc) {
     using L = Layout<D>;
     const int qd = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int row = qd * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(qd * 32) << 16);
-    const int i = row / p.G, head = kvh * p.G + row % p.G;
+    const uint32_t ts = trow + 128u * w, to = trow + L::kO + 128u * w;
+    const int r = row / p.G, head = kvh * p.G + row % p.G;
+    const int i = w * p.nt + r;  // query of the CTA
     const bool there = row < p.G * p.nt && i < tl.nq;
-    const int see = min(tl.kend, max(0, p.causal ? tl.see0 + i : tl.kend));
-    float m = -INFINITY, l = 0.f;
+    const int see = p.causal ? min(tl.Lk, max(0, tl.see0 + i)) : tl.Lk;
+    const int nkb = n[w];
+    // This tile reads the CTA's last value block first of the two (the issuer's
+    // order): it zeroes the rows behind the last key.
+    const bool clears = w == 0 ? n[0] == blocks : n[0] < blocks;
+    float m = -INFINITY;  // of the raw scores
+    float l = 0.f;
     for (int j = 0; j < nkb; ++j) {
-        if (!mbar_wait_warp<false>(bars.s_full(), (uint32_t)j & 1u, wc)) return;
+        if (!mbar_wait_warp<false>(bars.s_full(w), (uint32_t)j & 1u, wc)) return;
         tc_fence_after();
-        float s[kRows];
+        uint32_t s[kRows];
 #pragma unroll
-        for (int c0 = 0; c0 < kRows; c0 += 32) {
-            uint32_t r[32];
-            tmem_ld_cols(trow + (uint32_t)c0, 32, r);
+        for (int c0 = 0; c0 < kRows; c0 += 32) tmem_ld32_async(ts + (uint32_t)c0, s + c0);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) s[c0 + c] = __uint_as_float(r[c]);
-        }
-        tc_fence_before();
-        mbar_arrive(bars.s_free());
+        for (int c0 = 0; c0 < kRows; c0 += 32) tmem_ld_wait32(s + c0);
         const int kvalid = see - j * kRows;
-        float mx = -INFINITY;
+        if (__any_sync(0xffffffffu, kvalid < kRows)) {
 #pragma unroll
-        for (int c = 0; c < kRows; ++c) {
-            s[c] = c < kvalid ? s[c] * p.scale_log2 : -INFINITY;
-            mx = fmaxf(mx, s[c]);
+            for (int c = 0; c < kRows; ++c)
+                if (c >= kvalid) s[c] = 0xff800000u;  // -inf
         }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            mx[c] = fmaxf(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+#pragma unroll
+        for (int c = 8; c < kRows; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         float f = 1.f;
-        if (mx > m + 8.f) {
-            if (m != -INFINITY) f = exp2f(m - mx);
-            m = mx;
+        if ((top - m) * p.scale_log2 > 8.f) {  // (also the first block's, from -inf)
+            if (m != -INFINITY) f = exp2_fast((m - top) * p.scale_log2);
+            m = top;
         }
-        const float ms = m == -INFINITY ? 0.f : m;
-        float sum = 0.f;
-        uint32_t pk[kRows / 2];
-#pragma unroll
-        for (int c = 0; c < kRows; c += 2) {
-            const float a = exp2f(s[c] - ms), b = exp2f(s[c + 1] - ms);
-            sum += a + b;
-            pk[c / 2] = nact_pack(a, b);
-        }
-        l = l * f + sum;
-        // P's buffer and O are free once the previous block's product is done
-        if (j > 0 && !mbar_wait_warp<false>(bars.o_done(), (uint32_t)(j - 1) & 1u, wc)) return;
-        tc_fence_after();
-        if (__any_sync(0xffffffffu, f != 1.f)) {
+        // O is whole up to the last block: S came after its product
+        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            l *= f;
             for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t r[32];
-                tmem_ld_cols(trow + 128u + (uint32_t)c0, 32, r);
+                uint32_t o[32];
+                tmem_ld32_async(to + (uint32_t)c0, o);
+                tmem_ld_wait32(o);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * f);
-                tmem_st_cols32(trow + 128u + (uint32_t)c0, r);
+                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                tmem_st32_async(to + (uint32_t)c0, o);
             }
         }
+        const float ms = m == -INFINITY ? 0.f : m * p.scale_log2;
+        const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), ms2 = f32x2(-ms, -ms);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int ch = 0; ch < kRows / 8; ++ch)
-            *reinterpret_cast<uint4 *>(smem + L::kP + (ch >> 3) * kAtom + row * 128 +
-                                       (((ch & 7) ^ (row & 7)) << 4)) =
-                make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
-        // values behind the last visible key become zeros (the last block alone)
-        const int left = tl.kend - j * kRows;
-        if (left < kRows) {
-            const int st = j % kStages;
-            if (!mbar_wait_warp<false>(bars.v_full(st), (uint32_t)(j / kStages) & 1u, wc)) return;
-            uint4 *v = reinterpret_cast<uint4 *>(smem + L::kV + st * L::kTile);
-            for (int e = left * 8 + row; e < kRows * 8; e += 128)
+        for (int h = 0; h < 2; ++h) {  // 64 keys, 32 columns of P at a time
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const int e = h * 64 + 2 * c;
+                float a, b;
+                f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2,
+                                      ms2), a, b);
+                a = exp2_fast(a);
+                b = exp2_fast(b);
+                sum[c & 1] = add_f32x2(sum[c & 1], f32x2(a, b));
+                pk[c] = nact_pack(a, b);
+            }
+            tmem_st32_async(ts + 32u * h, pk);
+        }
+        float s0, s1;
+        f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        // values behind the last key of the CTA become zeros (its last block alone)
+        if (clears && j == blocks - 1 && keys_cta - j * kRows < kRows) {
+            if (!mbar_wait_warp<false>(bars.full(fill_v(j)), bars.phase(fill_v(j)), wc)) return;
+            uint4 *v = reinterpret_cast<uint4 *>(smem + L::kRing +
+                                                 (fill_v(j) % L::kStages) * L::kTile);
+            for (int e = (keys_cta - j * kRows) * 8 + row; e < kRows * 8; e += 128)
 #pragma unroll
                 for (int a = 0; a < D / 64; ++a) v[a * (kAtom / 16) + e] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();  // read by the tensor core (async proxy)
         }
-        fence_proxy_async_smem();  // P and V are read by the tensor core (async proxy)
+        tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bars.p_full());
+        mbar_arrive(bars.p_full(w));
     }
     if (nkb > 0) {
-        if (!mbar_wait_warp<false>(bars.o_done(), (uint32_t)(nkb - 1) & 1u, wc)) return;
+        if (!mbar_wait_warp<false>(bars.o_full(w), 0u, wc)) return;
         tc_fence_after();
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -344,17 +390,18 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int kvh, int nkb, u
     float probe = 0.f;  // NaN once an output is not finite
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t r[32];
+        uint32_t acc[32];
         if (nkb > 0) {
-            tmem_ld_cols(trow + 128u + (uint32_t)c0, 32, r);
+            tmem_ld32_async(to + (uint32_t)c0, acc);
+            tmem_ld_wait32(acc);
         } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) r[c] = 0u;
+            for (int c = 0; c < 32; ++c) acc[c] = 0u;
         }
         float o[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-            o[c] = see > 0 ? __uint_as_float(r[c]) * inv : 0.f;
+            o[c] = see > 0 ? __uint_as_float(acc[c]) * inv : 0.f;
             probe = fmaf(o[c], 0.f, probe);
         }
         if (there) {
@@ -389,21 +436,20 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Bars bars{sbase + L::kBars};
+    const Bars<D> bars{sbase + L::kBars};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kBars + 240);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kBars + 244);
     if (threadIdx.x == 0) {
         mbar_init(bars.q_full(), 1);
-        mbar_init(bars.s_full(), 1);
-        mbar_init(bars.s_free(), 128);
-        mbar_init(bars.p_full(), 128);
-        mbar_init(bars.o_done(), 1);
         mbar_init(bars.drain(), 1);
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(bars.k_full(s), 1);
-            mbar_init(bars.k_empty(s), 1);
-            mbar_init(bars.v_full(s), 1);
-            mbar_init(bars.v_empty(s), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(bars.s_full(w), 1);
+            mbar_init(bars.p_full(w), 128);
+            mbar_init(bars.o_full(w), 1);
+        }
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bars.full(s), 1);
+            mbar_init(bars.empty(s), 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -411,8 +457,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
         tma_prefetch_desc(&mK);
         tma_prefetch_desc(&mV);
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), 256u);
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512u);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -421,24 +467,27 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{p.wait_ns, p.err, abort_flag, 0u};
     griddep_wait();
-    const int kvh = blockIdx.y;
-    const Tile tl = find_tile(p, blockIdx.x);
-    const int nkb = (tl.kend + kRows - 1) / kRows;
-    if (tl.nq > 0) {
-        if (warp == 0) {
-            if (lane == 0 && nkb > 0)
-                producer<D>(&mQ, &mK, &mV, p, tl, kvh, nkb, sbase, bars, wc);
-        } else if (warp == 1) {
-            if (lane == 0 && nkb > 0) issuer<D>(nkb, sbase, tmem, bars, wc);
-        } else {
-            softmax<D>(p, tl, kvh, nkb, smem, tmem, bars, wc);
+    const int kvh = blockIdx.x % p.Hkv;
+    const Tile tl = find_tile(p, blockIdx.x / p.Hkv);
+    const int keys[2] = {keys_of(p, tl, 0), keys_of(p, tl, 1)};
+    const int n[2] = {blocks_of(keys[0]), blocks_of(keys[1])};
+    const int keys_cta = max(keys[0], keys[1]), blocks = max(n[0], n[1]);
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        if (tl.nq > 0)
+            softmax<D>(p, tl, warp >> 2, kvh, n, blocks, keys_cta, smem, tmem, bars, wc);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (lane == 0 && blocks > 0) {
+            if (warp == 8) issuer<D>(n, blocks, sbase, tmem, bars, wc);
+            if (warp == 9) producer<D>(&mQ, &mK, &mV, p, tl, kvh, blocks, sbase, bars, wc);
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 256u);
+    if (warp == 8) tmem_dealloc(tmem, 512u);
 }
 
 template <int D>
@@ -459,6 +508,7 @@ cudaError_t launch(const PackedAttnSpec &s, const LaunchCtx &ctx) {
     a.n_seq = s.n_seq;
     a.total_q = s.total_q;
     a.total_k = s.total_k;
+    a.Hkv = s.Hkv;
     a.G = s.Hq / s.Hkv;
     a.nt = kRows / a.G;
     a.scale_log2 = s.scale * 1.4426950408889634f;
@@ -490,11 +540,17 @@ cudaError_t launch(const PackedAttnSpec &s, const LaunchCtx &ctx) {
         e = cudaFuncSetAttribute(packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  L::kSmem);
         if (e != cudaSuccess) return e;
+        // the register split waits forever on a launch with fewer
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, packed_attn_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    // at most this many tiles, whatever the lengths (the rest finds none)
-    const int tiles = (s.total_q + a.nt - 1) / a.nt + s.n_seq;
-    return launch_pdl(packed_attn_kernel<D>, dim3((unsigned)tiles, (unsigned)s.Hkv), dim3(kThreads),
+    // at most this many pairs of tiles, whatever the lengths (the rest finds none)
+    const int64_t pairs = ((int64_t)s.total_q + 2 * a.nt - 1) / (2 * a.nt) + s.n_seq;
+    if (pairs * s.Hkv > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_pdl(packed_attn_kernel<D>, dim3((unsigned)(pairs * s.Hkv)), dim3(kThreads),
                       L::kSmem, ctx, mQ, mK, mV, a);
 }
 

@@ -38,9 +38,9 @@
 #include <atomic>
 
 #include "norm_act.cuh"
-#include "ptx.cuh"
 #include "seq_dev.cuh"
 #include "seq_ops.h"
+#include "seq_ptx.cuh"
 
 namespace wanvae {
 namespace {
@@ -131,12 +131,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
         return *reinterpret_cast<const uint32_t *>(&h);
     }
     return nact_pack(lo, hi);
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // D: head width; Q8: e4m3 cache; NH: blocks of 8 query heads read together.

@@ -97,8 +97,9 @@ wanvae_status wanvae_packed_attention(const void *q, int64_t q_stride, const voi
     if (head_dim != 64 && head_dim != 128) return WANVAE_ERR_UNSUPPORTED;
     const int64_t G = n_heads / n_kv_heads;
     if (n_kv_heads > 4096 || G > 128) return WANVAE_ERR_UNSUPPORTED;
-    // tiles of 128 / G queries, one more a sequence, in one launch's grid
-    if ((total_q + 128 / G - 1) / (128 / G) + n_seq > INT32_MAX) return WANVAE_ERR_UNSUPPORTED;
+    // pairs of tiles of 128 / G queries, one more a sequence, of every kv head in one grid
+    if ((total_q / (2 * (128 / G)) + 1 + n_seq) * n_kv_heads > INT32_MAX)
+        return WANVAE_ERR_UNSUPPORTED;
     const int64_t wq = n_heads * head_dim, wk = n_kv_heads * head_dim;
     if (!stride_ok(q_stride, wq) || !stride_ok(out_stride, wq) || !stride_ok(k_stride, wk) ||
         !stride_ok(v_stride, wk))

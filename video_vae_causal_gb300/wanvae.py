@@ -391,42 +391,53 @@ def resblock_forward_static(x, params, y, cache=None, stream=None):
 
 
 # ------------------------------------------------------------------ sequences
+# These calls are short enough for their own overhead to count (a decoding
+# step's kernels take a few microseconds each), so the checks ask each tensor
+# for as little as they need.
 def _fit(where, ok):
     """Refuse a call whose tensors do not fit it."""
     if not ok:
         raise WanvaeError(ERR_INVALID_ARG, where)
 
 
-def _on_device(where, *tensors):
-    """Every tensor (None: absent) lies on the current device: its context is
-    the one that the library launches in."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise WanvaeError(ERR_INVALID_ARG, where)
-    here = torch.cuda.current_device()
+def _on_device(where, first, *tensors):
+    """The current device's index, if every tensor (None: absent) lies there: its
+    context is the one that the library launches in."""
+    here = first.get_device()
+    _fit(where, here >= 0 and here == torch.cuda.current_device())
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise WanvaeError(ERR_INVALID_ARG, where)
+    return here
 
 
 def _raw(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# The current stream's handle without a Stream object around it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _heads(where, t, dtype=torch.bfloat16):
-    """Token stride of [tokens, heads, D] whose tokens are each contiguous."""
-    _fit(where, t.dim() == 3 and t.dtype == dtype)
+def _raw_stream(stream, device):
+    return _current_raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _heads(where, t):
+    """Token stride of bf16 [tokens, heads, D] whose tokens are each contiguous."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise WanvaeError(ERR_INVALID_ARG, where)
     n, h, d = t.shape
-    _fit(where, (h == 1 or t.stride(1) == d) and (d == 1 or t.stride(2) == 1))
-    return t.stride(0) if n > 1 else max(t.stride(0), h * d)
+    sn, sh, sd = t.stride()
+    if (h > 1 and sh != d) or (d > 1 and sd != 1):
+        raise WanvaeError(ERR_INVALID_ARG, where)
+    return sn if n > 1 else max(sn, h * d)
 
 
 def _ints(where, t, *shape):
-    _fit(where, t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape)
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise WanvaeError(ERR_INVALID_ARG, where)
 
 
 def _ours(t, stream):
@@ -443,22 +454,23 @@ def packed_attention(q, k, v, cu_q, cu_k=None, out=None, causal=True, scale=None
     given); causal: the last query of a sequence sees all of its keys.  Rows of
     `out` behind the last sequence are left as they were."""
     where = "wanvae_packed_attention"
-    if cu_k is None:
-        cu_k = cu_q
-    n = cu_q.numel() - 1
     if out is None:
         out = _ours(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
-    _on_device(where, q, k, v, cu_q, cu_k, out)
+    dev = _on_device(where, q, k, v, cu_q, cu_k, out)
+    n = cu_q.numel() - 1
     _ints(where, cu_q, n + 1)
-    _ints(where, cu_k, n + 1)
+    if cu_k is None:
+        cu_k = cu_q
+    else:
+        _ints(where, cu_k, n + 1)
     qs, ks, vs, os_ = _heads(where, q), _heads(where, k), _heads(where, v), _heads(where, out)
-    _fit(where, out.shape == q.shape and k.shape == v.shape and q.shape[2] == k.shape[2])
-    Tq, Hq, D = q.shape
-    Tk, Hkv, _ = k.shape
+    shape, kshape = q.shape, k.shape
+    _fit(where, out.shape == shape and v.shape == kshape and shape[2] == kshape[2])
+    Tq, Hq, D = shape
     st = load().wanvae_packed_attention(
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, out.data_ptr(), os_,
-        cu_q.data_ptr(), cu_k.data_ptr(), n, Tq, Tk, Hq, Hkv, D,
-        D ** -0.5 if scale is None else scale, 1 if causal else 0, _raw_stream(stream))
+        cu_q.data_ptr(), cu_k.data_ptr(), n, Tq, kshape[0], Hq, kshape[1], D,
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, _raw_stream(stream, dev))
     _check(st, where)
     return out
 
@@ -483,6 +495,8 @@ class KVCache:
         self.desc = KvCacheDesc(_raw(k), _raw(v), _raw(k_exp), _raw(v_exp), n, self.page_size,
                                 self.heads, self.head_dim, E4M3 if quant else BF16)
         self.ref = ctypes.byref(self.desc)
+        self.device = k.get_device()
+        _fit(where, all(t is None or t.get_device() == self.device for t in self.tensors()))
 
     def tensors(self):
         return self.k, self.v, self.k_exp, self.v_exp
@@ -507,10 +521,12 @@ def kv_cache_append(cache, k, v, lens, page_table, cu_new=None, stream=None):
     int32 [n + 1]: sequence s has rows cu_new[s] .. cu_new[s + 1] - 1; None: one
     row a sequence.  page_table int32 [n, max_pages]."""
     where = "wanvae_kv_cache_append"
-    _on_device(where, k, v, lens, page_table, cu_new, *cache.tensors())
+    dev = _on_device(where, k, v, lens, page_table, cu_new)
     ks, vs = _heads(where, k), _heads(where, v)
-    _fit(where, k.shape == v.shape and k.shape[1:] == (cache.heads, cache.head_dim) and
-         page_table.dim() == 2)
+    T = k.shape[0]
+    shape = (T, cache.heads, cache.head_dim)
+    _fit(where, k.shape == shape and v.shape == shape and page_table.dim() == 2 and
+         cache.device == dev)
     n, max_pages = page_table.shape
     _ints(where, lens, n)
     _ints(where, page_table, n, max_pages)
@@ -518,7 +534,7 @@ def kv_cache_append(cache, k, v, lens, page_table, cu_new=None, stream=None):
         _ints(where, cu_new, n + 1)
     st = load().wanvae_kv_cache_append(cache.ref, k.data_ptr(), ks, v.data_ptr(), vs,
                                        lens.data_ptr(), page_table.data_ptr(), max_pages,
-                                       _raw(cu_new), n, k.shape[0], _raw_stream(stream))
+                                       _raw(cu_new), n, T, _raw_stream(stream, dev))
     _check(st, where)
 
 
@@ -531,16 +547,18 @@ def kv_cache_gather(cache, page_table, cu, k=None, v=None, total=None, stream=No
         _fit(where, k is None and v is None and total is not None)
         k, v = (_ours(torch.empty((total, cache.heads, cache.head_dim), dtype=torch.bfloat16,
                                   device=page_table.device), stream) for _ in range(2))
-    _on_device(where, k, v, cu, page_table, *cache.tensors())
+    dev = _on_device(where, k, v, cu, page_table)
     ks, vs = _heads(where, k), _heads(where, v)
-    _fit(where, k.shape == v.shape and k.shape[1:] == (cache.heads, cache.head_dim) and
-         page_table.dim() == 2)
+    T = k.shape[0]
+    shape = (T, cache.heads, cache.head_dim)
+    _fit(where, k.shape == shape and v.shape == shape and page_table.dim() == 2 and
+         cache.device == dev)
     n, max_pages = page_table.shape
     _ints(where, cu, n + 1)
     _ints(where, page_table, n, max_pages)
     st = load().wanvae_kv_cache_gather(cache.ref, page_table.data_ptr(), max_pages, cu.data_ptr(),
-                                       n, k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs,
-                                       _raw_stream(stream))
+                                       n, T, k.data_ptr(), ks, v.data_ptr(), vs,
+                                       _raw_stream(stream, dev))
     _check(st, where)
     return k, v
 
@@ -565,10 +583,12 @@ def paged_attention(q, cache, lens, page_table, out=None, workspace=None, scale=
         out = _ours(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
     if workspace is None:
         workspace = _ours(make_paged_attention_workspace(q, cache), stream)
-    _on_device(where, q, lens, page_table, out, workspace, *cache.tensors())
+    dev = _on_device(where, q, lens, page_table, out, workspace)
     qs, os_ = _heads(where, q), _heads(where, out)
-    _fit(where, out.shape == q.shape and q.shape[2] == cache.head_dim and page_table.dim() == 2)
-    n, Hq, D = q.shape
+    shape = q.shape
+    n, Hq, D = shape
+    _fit(where, out.shape == shape and D == cache.head_dim and page_table.dim() == 2 and
+         cache.device == dev)
     max_pages = page_table.shape[1]
     _ints(where, lens, n)
     _ints(where, page_table, n, max_pages)
@@ -576,7 +596,7 @@ def paged_attention(q, cache, lens, page_table, out=None, workspace=None, scale=
                                        page_table.data_ptr(), max_pages, n, Hq,
                                        D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
                                        workspace.data_ptr(), workspace.nbytes,
-                                       _raw_stream(stream))
+                                       _raw_stream(stream, dev))
     _check(st, where)
     return out
 
@@ -588,27 +608,29 @@ def gated_residual_norm(x, f, gamma_post=None, gate=None, gamma_pre=None, tokens
     or fp32, contiguous).  gate fp32 [G, C]: token i has row i // tokens_per_gate.
     Returns (y, n); n is None without gamma_pre."""
     where = "wanvae_gated_residual_norm"
-    _fit(where, x.dtype in (torch.bfloat16, torch.float32))
     if y is None:
         y = _ours(torch.empty_like(x), stream)
     if n is None and gamma_pre is not None:
         n = _ours(torch.empty_like(x), stream)
-    _on_device(where, x, f, gamma_post, gate, gamma_pre, y, n)
-    for t in (x, f, y, n):
-        _fit(where, t is None or (t.shape == x.shape and t.dtype == x.dtype and
-                                  t.is_contiguous()))
-    C = x.shape[-1]
+    dev = _on_device(where, x, f, gamma_post, gate, gamma_pre, y, n)
+    shape, dtype = x.shape, x.dtype
+    _fit(where, (dtype == torch.bfloat16 or dtype == torch.float32) and x.is_contiguous())
+    for t in (f, y, n):
+        if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+            raise WanvaeError(ERR_INVALID_ARG, where)
+    C = shape[-1]
     tokens = x.numel() // C if C else 0
     for t in (gamma_post, gamma_pre):
-        _fit(where, t is None or (t.dtype == torch.float32 and t.is_contiguous() and
-                                  t.shape == (C,)))
+        if t is not None and (t.dtype != torch.float32 or t.shape != (C,) or
+                              not t.is_contiguous()):
+            raise WanvaeError(ERR_INVALID_ARG, where)
     if gate is not None:
         _fit(where, gate.dtype == torch.float32 and gate.is_contiguous() and gate.dim() == 2 and
              gate.shape[1] == C and tokens_per_gate >= 1 and
              gate.shape[0] * tokens_per_gate >= tokens)
     st = load().wanvae_gated_residual_norm(
         x.data_ptr(), f.data_ptr(), _raw(gamma_post), _raw(gate), tokens_per_gate,
-        _raw(gamma_pre), y.data_ptr(), _raw(n), BF16 if x.dtype == torch.bfloat16 else F32,
-        tokens, C, residual_scale, eps, _raw_stream(stream))
+        _raw(gamma_pre), y.data_ptr(), _raw(n), BF16 if dtype == torch.bfloat16 else F32,
+        tokens, C, residual_scale, eps, _raw_stream(stream, dev))
     _check(st, where)
     return y, n
