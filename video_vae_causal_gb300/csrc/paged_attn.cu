@@ -7,7 +7,7 @@
 // the G query heads that share it, so the work is G multiply-adds a cache
 // byte or less and the bound is HBM.
 //
-// Split.  The rows of one (sequence, kv head) are cut into units of 64; the
+// Split.  The rows of one (sequence, kv head) are cut into units of 64 or 128; the
 // units of the whole batch, laid end to end, are dealt to the CTAs in equal
 // contiguous shares, so a ragged batch and a single long sequence load every
 // multiprocessor alike.  A share may begin or end inside an item: then its
@@ -16,7 +16,7 @@
 // kernel joins them in the order of the CTAs.  Which CTA left what follows from the
 // lengths alone, so nothing is counted, reset or raced for.
 //
-// A warp takes 16 rows of a unit.  Its threads copy (cp.async) exactly the
+// A warp takes 16 or 32 rows of a unit.  Its threads copy (cp.async) exactly the
 // bytes that they will multiply: thread (g, t) = (lane / 4, lane % 4) needs, as the
 // B operand of S = Q K^T, a quarter of key rows g and g + 8, and as the A
 // operand of O^T = V^T P^T an eighth of value rows 2t, 2t + 1, 2t + 8 and
@@ -46,7 +46,6 @@ namespace wanvae {
 namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
-constexpr int kUnit = 16 * kWarps;  // cache rows of a unit
 constexpr int kMaxCtas = 640;       // CTAs of a launch (sizes the workspace)
 
 struct PagedArgs {
@@ -73,13 +72,17 @@ __device__ __forceinline__ int seq_len(const PagedArgs &p, int b, bool tell) {
     if (tell) atomicOr(p.err, kDevErrAlign);
     return len < 0 ? 0 : (int)most;
 }
-__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+template <int kUnit>
+__device__ __forceinline__ int units_of(int len) {
+    return (len + kUnit - 1) / kUnit;
+}
 
 // Units before sequence b (all of them for b = n_seq) of one head; whole warp.
+template <int kUnit>
 __device__ __forceinline__ int units_before(const PagedArgs &p, int b) {
     const int lane = threadIdx.x & 31;
     int n = 0;
-    for (int i = lane; i < b; i += 32) n += units_of(seq_len(p, i, false));
+    for (int i = lane; i < b; i += 32) n += units_of<kUnit>(seq_len(p, i, false));
     return __reduce_add_sync(0xffffffffu, n);
 }
 
@@ -91,8 +94,16 @@ __device__ __forceinline__ int share_of(int total, int unit, int ctas) {
 }
 
 template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool there) {
-    const int n = there ? kBytes : 0;  // bytes that are read; the rest is zeros
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    if (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// Same, or zeros where the source is not there.
+template <int kBytes>
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void *src, bool there) {
+    const int n = there ? kBytes : 0;  // bytes that are read
     if (kBytes == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                      : "memory");
@@ -141,36 +152,50 @@ struct Shape {
     static constexpr int KC = RB / 64;                   // 16-byte pieces of a key row, a thread
     static constexpr int VB = RB / 8 < 16 ? 8 : 16;      // bytes of a value piece
     static constexpr int VC = RB / 8 / VB;               // pieces of a value row, a thread
-    static constexpr int kStages = RB >= 256 ? 3 : 4;
-    static constexpr int kWarpStage = 32 * RB;           // bytes of a warp's 16 rows, k and v
-    static constexpr int kExpOff = kStages * kWarps * kWarpStage;  // 32 bytes a warp and stage
-    static constexpr int kMetaOff = kExpOff + kStages * kWarps * 32;
-    static constexpr int kJoinOff = (kMetaOff + kStages * kWarps * 4 + 15) / 16 * 16;
-    static constexpr int kJoinWarp = (D + D / 16) * 8;   // floats of a warp's 8 heads
-    static constexpr int kMlOff = kJoinOff + kWarps * NH * kJoinWarp * 4;
+    // Groups of 16 rows of a warp's turn: two share one maximum and give the
+    // tensor core twice the independent products; rows of 256 bytes take one
+    // so that three CTAs' queues fit a multiprocessor.
+    static constexpr int NG = RB >= 256 ? 1 : 2;
+    static constexpr int kUnit = 16 * NG * kWarps;       // cache rows of a unit
+    static constexpr int kStages = RB == 64 ? 4 : 2;
+    static constexpr int kGroup = 32 * RB;               // bytes of a group, k and v
+    static constexpr int kWarpStage = NG * kGroup;
+    static constexpr int kExpOff = kStages * kWarps * kWarpStage;  // 32 bytes a group
+    static constexpr int kMetaOff = kExpOff + kStages * kWarps * NG * 32;
+    static constexpr int kMlOff = kMetaOff + kStages * kWarps * 4;
     static constexpr int kSmem = kMlOff + kWarps * NH * 8 * 8;
+    // a warp's outputs wait for the join in its part of the stage just read:
+    // [D][8] floats for each 8 heads, 8 more behind every 16 rows where there is
+    // room (bank conflicts)
+    static constexpr int kPad = (D + D / 16) * 8 * 4 * NH <= kWarpStage ? 8 : 0;
+    static constexpr int kJoinHeads = (D * 8 + D / 16 * kPad);  // floats of 8 heads
+    static_assert(kJoinHeads * 4 * NH <= kWarpStage, "join buffer");
 };
 
 // Where a share stands: unit u of the U units of (sequence b, head block hh).
+template <int kUnit>
 struct Cursor {
     int b, hh, u, U, len;
-    __device__ __forceinline__ void next(const PagedArgs &p, int HH) {
-        if (++u < U) return;
+    // On to the next unit; true where the item changed.
+    __device__ __forceinline__ bool next(const PagedArgs &p, int HH) {
+        if (++u < U) return false;
         u = 0;
-        if (++hh < HH) return;
+        if (++hh < HH) return true;
         hh = 0;
         do {
-            if (++b >= p.n_seq) return;
+            if (++b >= p.n_seq) return true;
             len = seq_len(p, b, false);
-            U = units_of(len);
+            U = units_of<kUnit>(len);
         } while (U == 0);
+        return true;
     }
 };
 
 template <int D, bool Q8, int NH>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 paged_attn_kernel(const PagedArgs p) {
     using S = Shape<D, Q8, NH>;
+    constexpr int NG = S::NG;
     constexpr int kSteps = D / 16;  // 16-wide steps along D of a score; 16-row tiles of O^T
     extern __shared__ __align__(16) uint8_t smem[];
     griddep_launch_dependents();
@@ -180,17 +205,19 @@ paged_attn_kernel(const PagedArgs p) {
     const int HH = p.H * p.HB;
 
     // this CTA's share
-    const int total = units_before(p, p.n_seq) * HH;
+    const int total = units_before<S::kUnit>(p, p.n_seq) * HH;
     const int ctas = min((int)gridDim.x, total);  // no share is empty
     if ((int)blockIdx.x >= ctas) return;
     const int u0 = share_begin(total, blockIdx.x, ctas);
     const int u1 = share_begin(total, blockIdx.x + 1, ctas);
-    Cursor at;  // the unit to compute next
+    Cursor<S::kUnit> at;  // the unit to compute next
     {
         int b0 = 0, before = 0;  // (in units of one head)
         while (true) {
             const int i = b0 + lane;
-            const int U = i < p.n_seq ? units_of(seq_len(p, i, blockIdx.x == 0 && warp == 0)) : 0;
+            const int U = i < p.n_seq
+                              ? units_of<S::kUnit>(seq_len(p, i, blockIdx.x == 0 && warp == 0))
+                              : 0;
             int incl = U;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -216,53 +243,82 @@ paged_attn_kernel(const PagedArgs p) {
 
     const uint32_t base = smem_u32(smem);
     int *meta = reinterpret_cast<int *>(smem + S::kMetaOff);
-    // ---- copies: `ahead` is the unit to copy next, `page` its page (loaded one unit early)
-    Cursor ahead = at;
+    // ---- copies: `ahead` is the unit to copy next, `page` its pages (loaded one
+    // unit early), `kvh` its kv head
+    Cursor<S::kUnit> ahead = at;
     int left = u1 - u0;  // units not yet copied
-    auto find_page = [&]() -> int {
-        const int tok = ahead.u * kUnit + warp * 16;
-        if (tok >= ahead.len) return -1;
-        return __ldg(p.table + (int64_t)ahead.b * p.max_pages + (tok >> p.log2_page));
+    int kvh_ahead = ahead.hh / p.HB;
+    int page[NG];
+    auto find_pages = [&]() {
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const int tok = ahead.u * S::kUnit + (warp * NG + i) * 16;
+            page[i] = -1;
+            if (tok < ahead.len)
+                page[i] = __ldg(p.table + (int64_t)ahead.b * p.max_pages + (tok >> p.log2_page));
+        }
     };
-    int page = find_page();
+    find_pages();
     auto copy = [&](int stage) {
         if (left > 0) {
-            const int tok = ahead.u * kUnit + warp * 16;
-            int rows = min(max(ahead.len - tok, 0), 16);
-            if ((unsigned)page >= (unsigned)p.n_pages) {
-                if (rows && lane == 0) atomicOr(p.err, kDevErrAlign);
-                rows = 0;
+            int told = 0;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const int tok = ahead.u * S::kUnit + (warp * NG + i) * 16;
+                int rows = min(max(ahead.len - tok, 0), 16);
+                if ((unsigned)page[i] >= (unsigned)p.n_pages) {
+                    if (rows && lane == 0) atomicOr(p.err, kDevErrAlign);
+                    rows = 0;
+                }
+                told |= rows << (8 * i);
+                const int64_t row = rows ? ((((int64_t)page[i] * p.H + kvh_ahead) << p.log2_page) +
+                                            (tok & ((1 << p.log2_page) - 1)))
+                                         : 0;
+                const uint32_t dst = base + (uint32_t)((stage * kWarps + warp) * S::kWarpStage +
+                                                       i * S::kGroup);
+                const uint32_t kd = dst + lane * 16, vd = dst + 2 * S::KC * 512 + lane * S::VB;
+                const uint8_t *kr = p.k + row * S::RB + g * S::RB + 16 * t;
+                const uint8_t *vr = p.v + row * S::RB + 2 * t * S::RB + g * S::VB;
+                if (rows == 16) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < S::KC; ++c)
+                            cp_async<16>(kd + (j * S::KC + c) * 512, kr + 8 * j * S::RB + 64 * c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int c = 0; c < S::VC; ++c)
+                            cp_async<S::VB>(vd + (j * S::VC + c) * (32 * S::VB),
+                                            vr + ((j & 1) + 8 * (j >> 1)) * S::RB + c * 8 * S::VB);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < S::KC; ++c) {
+                            const bool in = 8 * j + g < rows;
+                            cp_async_part<16>(kd + (j * S::KC + c) * 512,
+                                              in ? kr + 8 * j * S::RB + 64 * c : p.k, in);
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int c = 0; c < S::VC; ++c) {
+                            const int r = (j & 1) + 8 * (j >> 1);
+                            const bool in = 2 * t + r < rows;
+                            cp_async_part<S::VB>(vd + (j * S::VC + c) * (32 * S::VB),
+                                                 in ? vr + r * S::RB + c * 8 * S::VB : p.v, in);
+                        }
+                }
+                if (Q8 && lane < 2)
+                    cp_async_part<16>(base + S::kExpOff +
+                                          ((stage * kWarps + warp) * NG + i) * 32 + lane * 16,
+                                      (lane ? p.v_exp : p.k_exp) + row, rows > 0);
             }
-            if (lane == 0) meta[stage * kWarps + warp] = rows;
-            const int64_t row = rows ? ((((int64_t)page * p.H + ahead.hh / p.HB) << p.log2_page) +
-                                        (tok & ((1 << p.log2_page) - 1)))
-                                     : 0;
-            const uint32_t dst = base + (uint32_t)((stage * kWarps + warp) * S::kWarpStage);
-            const uint8_t *kr = p.k + row * S::RB, *vr = p.v + row * S::RB;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = 8 * j + g;
-#pragma unroll
-                for (int c = 0; c < S::KC; ++c)
-                    cp_async<16>(dst + (j * S::KC + c) * 512 + lane * 16,
-                                 r < rows ? kr + r * S::RB + 64 * c + 16 * t : p.k, r < rows);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = 2 * t + (j & 1) + 8 * (j >> 1);
-#pragma unroll
-                for (int c = 0; c < S::VC; ++c)
-                    cp_async<S::VB>(dst + 2 * S::KC * 512 +
-                                        (j * S::VC + c) * (32 * S::VB) + lane * S::VB,
-                                    r < rows ? vr + r * S::RB + c * 8 * S::VB + g * S::VB : p.v,
-                                    r < rows);
-            }
-            if (Q8 && lane < 2)
-                cp_async<16>(base + S::kExpOff + (stage * kWarps + warp) * 32 + lane * 16,
-                             (lane ? p.v_exp : p.k_exp) + (rows ? row : 0), rows > 0);
+            if (lane == 0) meta[stage * kWarps + warp] = told;
             if (--left > 0) {
-                ahead.next(p, HH);
-                page = find_page();
+                if (ahead.next(p, HH)) kvh_ahead = ahead.hh / p.HB;
+                find_pages();
             }
         }
         cp_async_commit();  // (an empty group keeps the count)
@@ -341,158 +397,195 @@ paged_attn_kernel(const PagedArgs p) {
             copy(stage == 0 ? S::kStages - 1 : stage - 1);
             const uint8_t *src = smem + (stage * kWarps + warp) * S::kWarpStage;
             const int rows = meta[stage * kWarps + warp];
-            // S = Q K^T for rows 8 j + 2 t, + 1 and heads g, g + 8
-            float sc[2][4] = {};
+            // S = Q K^T for rows 8 j + 2 t, + 1 of a group and heads g, g + 8
+            float sc[NG][2][4] = {};
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int c = 0; c < S::KC; ++c) {
+                uint4 w4[NG][2];
 #pragma unroll
-                for (int c = 0; c < S::KC; ++c) {
-                    const uint4 w4 = *reinterpret_cast<const uint4 *>(
-                        src + (j * S::KC + c) * 512 + lane * 16);
-                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-                    constexpr int kPiece = Q8 ? 4 : 2;  // steps of a piece
+                for (int i = 0; i < NG; ++i)
 #pragma unroll
-                    for (int k = 0; k < kPiece; ++k) {
-                        const int s = c * kPiece + k;
-                        const uint32_t b0 = Q8 ? e4m3x2_to_f16x2(w[k % 4]) : w[(2 * k) % 4];
-                        const uint32_t b1 = Q8 ? e4m3x2_to_f16x2(w[k % 4] >> 16)
-                                               : w[(2 * k + 1) % 4];
-                        mma_16816<Q8>(sc[j], qa[s][0][0], NH > 1 ? qa[s][0][NH - 1] : 0u,
-                                      qa[s][1][0], NH > 1 ? qa[s][1][NH - 1] : 0u, b0, b1);
-                    }
-                }
-            // the rows' scales: keys' as factors, values' as exponents
-            float kf[2][2], ve[2][2];
+                    for (int j = 0; j < 2; ++j)
+                        w4[i][j] = *reinterpret_cast<const uint4 *>(
+                            src + i * S::kGroup + (j * S::KC + c) * 512 + lane * 16);
+                constexpr int kPiece = Q8 ? 4 : 2;  // steps of a piece
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int k = 0; k < kPiece; ++k) {
+                    const int s = c * kPiece + k;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    kf[j][c] = 1.f;
-                    ve[j][c] = 0.f;
-                }
-            if (Q8) {
-                const uint8_t *ex = smem + S::kExpOff + (stage * kWarps + warp) * 32;
+                    for (int i = 0; i < NG; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t kx = *reinterpret_cast<const uint16_t *>(ex + 8 * j + 2 * t);
-                    const uint32_t vx = *reinterpret_cast<const uint16_t *>(ex + 16 + 8 * j + 2 * t);
-                    kf[j][0] = __uint_as_float((kx & 0xffu) << 23);
-                    kf[j][1] = __uint_as_float((kx >> 8) << 23);
-                    ve[j][0] = (float)(int)(vx & 0xffu) - 127.f;
-                    ve[j][1] = (float)(int)(vx >> 8) - 127.f;
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t w[4] = {w4[i][j].x, w4[i][j].y, w4[i][j].z, w4[i][j].w};
+                            const uint32_t b0 = Q8 ? e4m3x2_to_f16x2(w[k % 4]) : w[(2 * k) % 4];
+                            const uint32_t b1 = Q8 ? e4m3x2_to_f16x2(w[k % 4] >> 16)
+                                                   : w[(2 * k + 1) % 4];
+                            mma_16816<Q8>(sc[i][j], qa[s][0][0], NH > 1 ? qa[s][0][NH - 1] : 0u,
+                                          qa[s][1][0], NH > 1 ? qa[s][1][NH - 1] : 0u, b0, b1);
+                        }
                 }
             }
-            uint32_t pb[NH][2];
+            // the rows' scales: keys' as factors, values' as exponents
+            float kf[NG][2][2], ve[NG][2][2];
 #pragma unroll
-            for (int i = 0; i < NH; ++i) {
-                float s[2][2], mx = -INFINITY;
+            for (int i = 0; i < NG; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < 2; ++j) {
+                    kf[i][j][0] = kf[i][j][1] = 1.f;
+                    ve[i][j][0] = ve[i][j][1] = 0.f;
+                    if (!Q8) continue;
+                    const uint8_t *ex =
+                        smem + S::kExpOff + ((stage * kWarps + warp) * NG + i) * 32 + 8 * j + 2 * t;
+                    const uint32_t kx = *reinterpret_cast<const uint16_t *>(ex);
+                    const uint32_t vx = *reinterpret_cast<const uint16_t *>(ex + 16);
+                    kf[i][j][0] = __uint_as_float((kx << 23) & 0x7f800000u);
+                    kf[i][j][1] = __uint_as_float((kx << 15) & 0x7f800000u);
+                    // 2^23 + code, less 2^23 + 127
+                    ve[i][j][0] = __uint_as_float(__byte_perm(vx, 0x4b000000u, 0x7440)) - 8388735.f;
+                    ve[i][j][1] = __uint_as_float(__byte_perm(vx, 0x4b000000u, 0x7441)) - 8388735.f;
+                }
+            uint32_t pb[NH][NG][2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        s[j][c] = sc[j][2 * i + c] * (qs[i] * kf[j][c]);
-                        if (8 * j + 2 * t + c >= rows) s[j][c] = -INFINITY;
-                        mx = fmaxf(mx, s[j][c] + ve[j][c]);
-                    }
+            for (int h = 0; h < NH; ++h) {
+                float s[NG][2][2], mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            s[i][j][c] = sc[i][j][2 * h + c] * (qs[h] * kf[i][j][c]);
+                if (rows != (NG == 2 ? 0x1010 : 0x10)) {
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (8 * j + 2 * t + c >= ((rows >> (8 * i)) & 0xff))
+                                    s[i][j][c] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        mx = max3(mx, s[i][j][0] + ve[i][j][0], s[i][j][1] + ve[i][j][1]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[i], mx);
-                const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 0
-                if (__any_sync(0xffffffffu, mn > m[i])) {
-                    const float f = exp2_fast(m[i] - ms);
-                    m[i] = mn;
-                    l[i] *= f;
+                // the maximum moves only by more than 2^4: weights stay below 16,
+                // their sums below fp16's products' fp32 range, and O is seldom rescaled
+                if (__any_sync(0xffffffffu, mx > m[h] + 4.f)) {
+                    const float mn = fmaxf(m[h], mx);
+                    const float f = mn == -INFINITY ? 0.f : exp2_fast(m[h] - mn);
+                    m[h] = mn;
+                    l[h] *= f;
                     const float f0 = __shfl_sync(0xffffffffu, f, 8 * t);
                     const float f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
-                        o[i][k][0] *= f0;
-                        o[i][k][1] *= f1;
-                        o[i][k][2] *= f0;
-                        o[i][k][3] *= f1;
+                        o[h][k][0] *= f0;
+                        o[h][k][1] *= f1;
+                        o[h][k][2] *= f0;
+                        o[h][k][3] *= f1;
                     }
                 }
-                float w[2][2];
+                const float ms = m[h] == -INFINITY ? 0.f : m[h];  // nothing seen yet: weights 0
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int i = 0; i < NG; ++i) {
+                    float w[2][2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float e = exp2_fast(s[j][c] - ms);
-                        l[i] += e;
-                        w[j][c] = Q8 ? exp2_fast(s[j][c] + ve[j][c] - ms) : e;
-                    }
-                pb[i][0] = pack16<Q8>(w[0][0], w[0][1]);
-                pb[i][1] = pack16<Q8>(w[1][0], w[1][1]);
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float x = s[i][j][c] - ms;
+                            const float e = exp2_fast(x);
+                            l[h] += e;
+                            w[j][c] = Q8 ? exp2_fast(x + ve[i][j][c]) : e;
+                        }
+                    pb[h][i][0] = pack16<Q8>(w[0][0], w[0][1]);
+                    pb[h][i][1] = pack16<Q8>(w[1][0], w[1][1]);
+                }
             }
             // O^T += V^T P^T: tile s holds elements 2 s (rows g) and 2 s + 1
             // (rows g + 8) of this thread's piece of the value rows
-            const uint8_t *vsrc = src + 2 * S::KC * 512 + lane * S::VB;
 #pragma unroll
-            for (int c = 0; c < S::VC; ++c) {
-                uint32_t r[4][S::VB / 4];
+            for (int i = 0; i < NG; ++i) {
+                const uint8_t *vsrc = src + i * S::kGroup + 2 * S::KC * 512 + lane * S::VB;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint8_t *a = vsrc + (j * S::VC + c) * (32 * S::VB);
-                    if (S::VB == 16) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(a);
-                        r[j][0] = x.x;
-                        r[j][1] = x.y;
-                        r[j][2 % (S::VB / 4)] = x.z;
-                        r[j][3 % (S::VB / 4)] = x.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(a);
-                        r[j][0] = x.x;
-                        r[j][1] = x.y;
-                    }
-                }
+                for (int c = 0; c < S::VC; ++c) {
+                    uint32_t r[4][S::VB / 4];
 #pragma unroll
-                for (int x = 0; x < S::VB / 4; ++x) {
-                    if (Q8) {
-                        const uint32_t lo0 = __byte_perm(r[0][x], r[1][x], 0x5140);
-                        const uint32_t hi0 = __byte_perm(r[0][x], r[1][x], 0x7362);
-                        const uint32_t lo1 = __byte_perm(r[2][x], r[3][x], 0x5140);
-                        const uint32_t hi1 = __byte_perm(r[2][x], r[3][x], 0x7362);
-                        const uint32_t a0 = e4m3x2_to_f16x2(lo0), a1 = e4m3x2_to_f16x2(lo0 >> 16);
-                        const uint32_t a2 = e4m3x2_to_f16x2(lo1), a3 = e4m3x2_to_f16x2(lo1 >> 16);
-                        const uint32_t c0 = e4m3x2_to_f16x2(hi0), c1 = e4m3x2_to_f16x2(hi0 >> 16);
-                        const uint32_t c2 = e4m3x2_to_f16x2(hi1), c3 = e4m3x2_to_f16x2(hi1 >> 16);
-#pragma unroll
-                        for (int i = 0; i < NH; ++i) {
-                            mma_16816<Q8>(o[i][(2 * x) % kSteps], a0, a1, a2, a3, pb[i][0], pb[i][1]);
-                            mma_16816<Q8>(o[i][(2 * x + 1) % kSteps], c0, c1, c2, c3, pb[i][0],
-                                          pb[i][1]);
+                    for (int j = 0; j < 4; ++j) {
+                        const uint8_t *a = vsrc + (j * S::VC + c) * (32 * S::VB);
+                        if (S::VB == 16) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(a);
+                            r[j][0] = x.x;
+                            r[j][1] = x.y;
+                            r[j][2 % (S::VB / 4)] = x.z;
+                            r[j][3 % (S::VB / 4)] = x.w;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(a);
+                            r[j][0] = x.x;
+                            r[j][1] = x.y;
                         }
-                    } else {
-                        const uint32_t a0 = __byte_perm(r[0][x], r[1][x], 0x5410);
-                        const uint32_t a1 = __byte_perm(r[0][x], r[1][x], 0x7632);
-                        const uint32_t a2 = __byte_perm(r[2][x], r[3][x], 0x5410);
-                        const uint32_t a3 = __byte_perm(r[2][x], r[3][x], 0x7632);
+                    }
 #pragma unroll
-                        for (int i = 0; i < NH; ++i)
-                            mma_16816<Q8>(o[i][(c * 4 + x) % kSteps], a0, a1, a2, a3, pb[i][0],
-                                          pb[i][1]);
+                    for (int x = 0; x < S::VB / 4; ++x) {
+                        if (Q8) {
+                            const uint32_t lo0 = __byte_perm(r[0][x], r[1][x], 0x5140);
+                            const uint32_t hi0 = __byte_perm(r[0][x], r[1][x], 0x7362);
+                            const uint32_t lo1 = __byte_perm(r[2][x], r[3][x], 0x5140);
+                            const uint32_t hi1 = __byte_perm(r[2][x], r[3][x], 0x7362);
+                            const uint32_t a0 = e4m3x2_to_f16x2(lo0);
+                            const uint32_t a1 = e4m3x2_to_f16x2(lo0 >> 16);
+                            const uint32_t a2 = e4m3x2_to_f16x2(lo1);
+                            const uint32_t a3 = e4m3x2_to_f16x2(lo1 >> 16);
+                            const uint32_t c0 = e4m3x2_to_f16x2(hi0);
+                            const uint32_t c1 = e4m3x2_to_f16x2(hi0 >> 16);
+                            const uint32_t c2 = e4m3x2_to_f16x2(hi1);
+                            const uint32_t c3 = e4m3x2_to_f16x2(hi1 >> 16);
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) {
+                                mma_16816<Q8>(o[h][(2 * x) % kSteps], a0, a1, a2, a3, pb[h][i][0],
+                                              pb[h][i][1]);
+                                mma_16816<Q8>(o[h][(2 * x + 1) % kSteps], c0, c1, c2, c3,
+                                              pb[h][i][0], pb[h][i][1]);
+                            }
+                        } else {
+                            const uint32_t a0 = __byte_perm(r[0][x], r[1][x], 0x5410);
+                            const uint32_t a1 = __byte_perm(r[0][x], r[1][x], 0x7632);
+                            const uint32_t a2 = __byte_perm(r[2][x], r[3][x], 0x5410);
+                            const uint32_t a3 = __byte_perm(r[2][x], r[3][x], 0x7632);
+#pragma unroll
+                            for (int h = 0; h < NH; ++h)
+                                mma_16816<Q8>(o[h][(c * 4 + x) % kSteps], a0, a1, a2, a3,
+                                              pb[h][i][0], pb[h][i][1]);
+                        }
                     }
                 }
             }
             stage = stage + 1 == S::kStages ? 0 : stage + 1;
         }
 
-        // ---- join the warps, then leave the result or a partial one
-        float *join = reinterpret_cast<float *>(smem + S::kJoinOff);
+        // ---- join the warps, then leave the result or a partial one.  A warp's
+        // outputs go to its part of the stage that it has just read (the next copy
+        // into it comes after the second barrier).
+        uint8_t *last = smem + (stage == 0 ? S::kStages - 1 : stage - 1) * kWarps * S::kWarpStage;
         float2 *ml = reinterpret_cast<float2 *>(smem + S::kMlOff);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             if (t == 0) ml[(warp * NH + i) * 8 + g] = make_float2(m[i], l[i]);
-            float *dst = join + (warp * NH + i) * S::kJoinWarp;
+            float *dst = reinterpret_cast<float *>(last + warp * S::kWarpStage) + i * S::kJoinHeads;
             constexpr int kEl = S::VB / S::EB;  // elements of a value piece
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 const int c = 2 * s / kEl, e = 2 * s % kEl;
                 const int d = c * 8 * kEl + g * kEl + e;
-                float *a = dst + d * 8 + (d >> 4) * 8 + 2 * t;
-                float *b = dst + (d + 1) * 8 + ((d + 1) >> 4) * 8 + 2 * t;
+                float *a = dst + d * 8 + (d >> 4) * S::kPad + 2 * t;
+                float *b = dst + (d + 1) * 8 + ((d + 1) >> 4) * S::kPad + 2 * t;
                 *reinterpret_cast<float2 *>(a) = make_float2(o[i][s][0], o[i][s][1]);
                 *reinterpret_cast<float2 *>(b) = make_float2(o[i][s][2], o[i][s][3]);
             }
@@ -513,7 +606,8 @@ paged_attn_kernel(const PagedArgs p) {
             for (int w = 0; w < kWarps; ++w) {
                 const float f = mw[w] == -INFINITY ? 0.f : exp2_fast(mw[w] - top);
                 sum += f * ml[(w * NH + i) * 8 + hr].y;
-                acc += f * join[(w * NH + i) * S::kJoinWarp + d * 8 + (d >> 4) * 8 + hr];
+                acc += f * reinterpret_cast<const float *>(last + w * S::kWarpStage)
+                               [i * S::kJoinHeads + d * 8 + (d >> 4) * S::kPad + hr];
             }
             if (whole) {
                 p.out[(int64_t)at.b * p.out_stride + (int64_t)(h0 + h) * D + d] =
@@ -535,47 +629,68 @@ paged_attn_kernel(const PagedArgs p) {
 
 // Joins the partial results of the items that were cut between CTAs, and
 // writes zeros for sequences without rows.  One block of D threads for each
-// (query head, sequence).
-template <int D>
+// (query head, sequence): the parts' weights side by side, then the sum of the
+// parts in their order.
+template <int D, int kUnit>
 __global__ void __launch_bounds__(D)
 paged_join_kernel(const PagedArgs p, int most_ctas, int block_heads) {
+    __shared__ float weight[kMaxCtas];
+    __shared__ float2 warp_ml[D / 32];
     griddep_launch_dependents();
     griddep_wait();
     const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
     __nv_bfloat16 *out = p.out + (int64_t)b * p.out_stride + (int64_t)h * D + d;
-    const int U = units_of(seq_len(p, b, false));
+    const int U = units_of<kUnit>(seq_len(p, b, false));
     if (U == 0) {
         *out = __float2bfloat16(0.f);
         return;
     }
     const int HH = p.H * p.HB;
     const int kvh = h / p.G, hb = (h % p.G) / block_heads, hr = (h % p.G) % block_heads;
-    const int total = units_before(p, p.n_seq) * HH;
+    const int total = units_before<kUnit>(p, p.n_seq) * HH;
     const int ctas = min(most_ctas, total);
-    const int i0 = units_before(p, b) * HH + (kvh * p.HB + hb) * U;
+    const int i0 = units_before<kUnit>(p, b) * HH + (kvh * p.HB + hb) * U;
     const int c0 = share_of(total, i0, ctas), c1 = share_of(total, i0 + U - 1, ctas);
     if (c0 == c1) return;  // one CTA held the whole item and wrote it
-    auto slot_of = [&](int c) {
-        return (2 * c + (share_begin(total, c, ctas) < i0 ? 1 : 0)) * block_heads + hr;
-    };
+    // the item lies in the first slot of its CTAs, but for one that began before it
+    const int s0 = 2 * c0 + (share_begin(total, c0, ctas) < i0 ? 1 : 0);
+    auto slot_of = [&](int c) { return (c == c0 ? s0 : 2 * c) * block_heads + hr; };
     float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c) top = fmaxf(top, p.part_ml[slot_of(c)].x);
-    float sum = 0.f, acc = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        const int s = slot_of(c);
-        const float2 ml = p.part_ml[s];
+    for (int c = c0 + d; c <= c1; c += D) top = fmaxf(top, p.part_ml[slot_of(c)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if ((d & 31) == 0) warp_ml[d >> 5].x = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) top = fmaxf(top, warp_ml[w].x);
+    float sum = 0.f;
+    for (int c = c0 + d; c <= c1; c += D) {
+        const float2 ml = p.part_ml[slot_of(c)];
         const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+        weight[c - c0] = f;
         sum += f * ml.y;
-        acc += f * p.part_o[(int64_t)s * D + d];
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if ((d & 31) == 0) warp_ml[d >> 5].y = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) sum += warp_ml[w].y;
+    float acc = weight[0] * p.part_o[(int64_t)slot_of(c0) * D + d];
+#pragma unroll 8
+    for (int c = c0 + 1; c <= c1; ++c) acc += weight[c - c0] * p.part_o[(int64_t)slot_of(c) * D + d];
     *out = __float2bfloat16(sum > 0.f || sum != sum ? acc / sum : 0.f);
 }
 
 int head_block(int G) { return G <= 8 ? 8 : 16; }
 
 template <int D, bool Q8, int NH>
-cudaError_t launch(const PagedArgs &a, int64_t most_units, const LaunchCtx &ctx) {
+cudaError_t launch(const PagedArgs &a, const LaunchCtx &ctx) {
     using S = Shape<D, Q8, NH>;
+    const int64_t most_units =
+        (((int64_t)a.max_pages << a.log2_page) + S::kUnit - 1) / S::kUnit * a.n_seq * a.H * a.HB;
+    if (most_units > INT32_MAX) return cudaErrorInvalidValue;
     auto *kern = paged_attn_kernel<D, Q8, NH>;
     // resident CTAs, and the shared-memory opt-in, once per device
     constexpr int kMaxDev = 64;
@@ -597,7 +712,7 @@ cudaError_t launch(const PagedArgs &a, int64_t most_units, const LaunchCtx &ctx)
         1, std::min<int64_t>(most_units, std::min(kMaxCtas, occ * ctx.num_sms)));
     e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), S::kSmem, ctx, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_join_kernel<D>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
+    return launch_pdl(paged_join_kernel<D, S::kUnit>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
                       dim3(D), 0, ctx, a, ctas, 8 * NH);
 }
 
@@ -636,17 +751,14 @@ cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t 
     a.part_ml = static_cast<float2 *>(workspace);
     a.part_o = reinterpret_cast<float *>(a.part_ml + rows);
     a.err = ctx.err;
-    const int64_t most = (((int64_t)max_pages << c.log2_page) + kUnit - 1) / kUnit * n_seq * c.H *
-                         a.HB;
-    if (most > INT32_MAX) return cudaErrorInvalidValue;
     if (c.D == 64) {
-        if (c.e4m3) return hb == 8 ? launch<64, true, 1>(a, most, ctx) : launch<64, true, 2>(a, most, ctx);
-        return hb == 8 ? launch<64, false, 1>(a, most, ctx) : launch<64, false, 2>(a, most, ctx);
+        if (c.e4m3) return hb == 8 ? launch<64, true, 1>(a, ctx) : launch<64, true, 2>(a, ctx);
+        return hb == 8 ? launch<64, false, 1>(a, ctx) : launch<64, false, 2>(a, ctx);
     }
     if (c.D == 128) {
         if (c.e4m3)
-            return hb == 8 ? launch<128, true, 1>(a, most, ctx) : launch<128, true, 2>(a, most, ctx);
-        return hb == 8 ? launch<128, false, 1>(a, most, ctx) : launch<128, false, 2>(a, most, ctx);
+            return hb == 8 ? launch<128, true, 1>(a, ctx) : launch<128, true, 2>(a, ctx);
+        return hb == 8 ? launch<128, false, 1>(a, ctx) : launch<128, false, 2>(a, ctx);
     }
     return cudaErrorInvalidValue;
 }
