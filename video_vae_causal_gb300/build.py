@@ -19,10 +19,10 @@ SOURCES = ["api.cu", "rmsnorm_silu.cu", "conv3d_tcgen05.cu", "conv3d_narrow.cu",
            "attn_tcgen05.cu", "conv3d_kernels_p1_n1.cu", "conv3d_kernels_p1_n2.cu",
            "conv3d_kernels_p2_n1.cu", "conv3d_kernels_p2_n2.cu", "conv3d_kernels_misc.cu",
            "conv3d_kernels_fuse.cu", "seq_api.cu", "packed_attn.cu", "paged_attn.cu",
-           "kv_cache.cu", "gated_norm.cu"]
+           "paged_attn_tc.cu", "kv_cache.cu", "gated_norm.cu"]
 DEPS = SOURCES + ["ptx.cuh", "kernels.h", "exports.map", "conv3d_tcgen05.cuh",
                   "conv3d_kernels.inc", "norm_act.cuh", "seq_ops.h", "seq_dev.cuh",
-                  "seq_ptx.cuh"]
+                  "seq_ptx.cuh", "paged_attn.cuh"]
 HEADER = os.path.join(ROOT, "include", "wanvae.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -8,29 +8,37 @@
 // byte or less and the bound is HBM.
 //
 // Split.  The rows of one (sequence, kv head) are cut into units of 64 or 128; the
-// units of the whole batch, laid end to end, are dealt to the CTAs in equal
-// contiguous shares, so a ragged batch and a single long sequence load every
-// multiprocessor alike.  A share may begin or end inside an item: then its
-// CTA leaves a partial result (the running maximum, the sum and the
-// unnormalised output) in the workspace, two slots a CTA, and a second small
-// kernel joins them in the order of the CTAs.  Which CTA left what follows from the
-// lengths alone, so nothing is counted, reset or raced for.
+// units of the whole batch, laid end to end, are dealt to the CTAs in contiguous
+// ranges: an equal share each, so a ragged batch and a single long sequence load
+// every multiprocessor alike, and of large batches the last tenth of each share apart,
+// for the CTA that is done first (multiprocessors differ by a tenth in the
+// bandwidth that they get).  A range may begin or end inside an item: then its
+// CTA leaves a partial result (the running maximum, the sum and the unnormalised
+// output) in the workspace, two slots a range, and a second small kernel joins them
+// in the ranges' order.  The ranges follow from the lengths alone, so neither
+// which CTA took one nor the order in which they end changes a bit.
 //
-// A warp takes 16 or 32 rows of a unit.  Its threads copy (cp.async) exactly the
-// bytes that they will multiply: thread (g, t) = (lane / 4, lane % 4) needs, as the
-// B operand of S = Q K^T, a quarter of key rows g and g + 8, and as the A
-// operand of O^T = V^T P^T an eighth of value rows 2t, 2t + 1, 2t + 8 and
-// 2t + 9.  The order of the elements along the summed dimension is free, so
-// these are whole 16-byte pieces; shared memory is a private queue of each
-// thread (no barrier, no bank conflict), kStages units deep.
+// A warp takes 16 or 32 rows of a unit, for which one lane starts two TMA loads of
+// 16 rows each (keys, values) into the warp's own queue, kStages turns deep; no
+// warp waits for another until an item ends.  Thread (g, t) = (lane / 4, lane % 4)
+// needs, as the B operand of S = Q K^T, a quarter of two key rows and, as the A operand
+// of O^T = V^T P^T, an eighth of four value rows.  The order of the elements along
+// the summed dimension is free, so these are whole 16-byte pieces, and the order of
+// the rows is chosen so that with TMA's swizzle eight lanes read eight banks' pieces
+// (rows of 128 bytes: column g of S is row g / 2 + 4 (g % 2)).
 //
-// 8-bit rows become fp16 exactly; queries become fp16 with a power of two taken
-// out so that the largest has exponent 14 (bf16's 8 bits fit in fp16's 11;
-// what falls below fp16's range is 2^-39 of the largest).  A key row's scale
-// multiplies its score; a value row's scale 2^e joins the exponent of its
-// weight, w_j = 2^(s_j + e_j - m) with m the running maximum of s_j + e_j, while the sum
-// takes 2^(s_j - m) in fp32, so that weights stay in fp16's upper range
-// whatever the scales are (weights round once, to 2^-12 relative).
+// 8-bit keys are multiplied as they are (an e4m3 MMA is four times the rate of a
+// 16-bit one, and needs no conversion): a query becomes two e4m3 terms, q 2^x =
+// a + b / 32 with a the nearest e4m3 value and b what is left, both exact for bf16's 8
+// bits down to 2^-14 of the query's largest element and within 2^-22 of it below
+// (x brings that element to exponent 7).  The second term takes the MMA's other
+// eight rows, which the heads leave free.  8-bit values become fp16 exactly, and
+// weights round once to fp16 (2^-12 relative): as two e4m3 terms small weights of
+// many rows would round alike.  A key row's scale multiplies its score; a value
+// row's scale 2^e joins the exponent of its weight, w_j = 2^(s_j + e_j - m) with m the
+// running maximum of s_j + e_j, while the sum takes 2^(s_j - m) in fp32, so that
+// weights stay in fp16's upper range whatever the scales are.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -38,86 +46,13 @@
 #include <atomic>
 
 #include "norm_act.cuh"
-#include "seq_dev.cuh"
-#include "seq_ops.h"
-#include "seq_ptx.cuh"
+#include "paged_attn.cuh"
 
 namespace wanvae {
 namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
-constexpr int kMaxCtas = 640;       // CTAs of a launch (sizes the workspace)
-
-struct PagedArgs {
-    const __nv_bfloat16 *q;
-    int64_t q_stride;
-    const uint8_t *k, *v, *k_exp, *v_exp;
-    int n_pages, log2_page, H;
-    const int32_t *table, *lens;
-    int max_pages, n_seq;
-    int G, HB;  // query heads of a kv head; blocks of heads that a kv head is read for
-    float scale_log2;
-    __nv_bfloat16 *out;
-    int64_t out_stride;
-    float *part_o;   // [2 CTAs][heads of a block][D]
-    float2 *part_ml; // [2 CTAs][heads of a block]: maximum, sum
-    unsigned *err;
-};
-
-// A sequence's length as far as the page table reaches.
-__device__ __forceinline__ int seq_len(const PagedArgs &p, int b, bool tell) {
-    const int len = __ldg(p.lens + b);
-    const int64_t most = (int64_t)p.max_pages << p.log2_page;
-    if (len >= 0 && len <= most) return len;
-    if (tell) atomicOr(p.err, kDevErrAlign);
-    return len < 0 ? 0 : (int)most;
-}
-template <int kUnit>
-__device__ __forceinline__ int units_of(int len) {
-    return (len + kUnit - 1) / kUnit;
-}
-
-// Units before sequence b (all of them for b = n_seq) of one head; whole warp.
-template <int kUnit>
-__device__ __forceinline__ int units_before(const PagedArgs &p, int b) {
-    const int lane = threadIdx.x & 31;
-    int n = 0;
-    for (int i = lane; i < b; i += 32) n += units_of<kUnit>(seq_len(p, i, false));
-    return __reduce_add_sync(0xffffffffu, n);
-}
-
-__device__ __forceinline__ int share_begin(int total, int cta, int ctas) {
-    return (int)((int64_t)total * cta / ctas);
-}
-__device__ __forceinline__ int share_of(int total, int unit, int ctas) {
-    return (int)((((int64_t)unit + 1) * ctas - 1) / total);
-}
-
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
-    if (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-// Same, or zeros where the source is not there.
-template <int kBytes>
-__device__ __forceinline__ void cp_async_part(uint32_t dst, const void *src, bool there) {
-    const int n = there ? kBytes : 0;  // bytes that are read
-    if (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n)
-                     : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kLeft>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
+constexpr int kJoinThreads = 256;
 
 // D += A B, 16 x 8 x 16, fp16 or bf16 in, fp32 out.
 template <bool F16>
@@ -147,106 +82,94 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // D: head width; Q8: e4m3 cache; NH: blocks of 8 query heads read together.
 template <int D, bool Q8, int NH>
 struct Shape {
-    static constexpr int EB = Q8 ? 1 : 2;                // bytes of an element
-    static constexpr int RB = D * EB;                    // bytes of a row
-    static constexpr int KC = RB / 64;                   // 16-byte pieces of a key row, a thread
-    static constexpr int VB = RB / 8 < 16 ? 8 : 16;      // bytes of a value piece
-    static constexpr int VC = RB / 8 / VB;               // pieces of a value row, a thread
-    // Groups of 16 rows of a warp's turn: two share one maximum and give the
-    // tensor core twice the independent products; rows of 256 bytes take one
-    // so that three CTAs' queues fit a multiprocessor.
+    static constexpr int EB = Q8 ? 1 : 2;            // bytes of an element
+    static constexpr int RB = D * EB;                // bytes of a row
+    static constexpr int SB = RB < 128 ? RB : 128;   // bytes of a row of a TMA box
+    static constexpr int NS = RB / SB;               // boxes of 16 rows
+    static constexpr int KC = RB / 64;               // 16-byte pieces of a key row, a thread
+    static constexpr int VB = RB / 8 < 16 ? 8 : 16;  // bytes of a value piece
+    static constexpr int VC = RB / 8 / VB;           // pieces of a value row, a thread
+    // Groups of 16 rows of a warp's turn, and resident CTAs.
     static constexpr int NG = RB >= 256 ? 1 : 2;
-    static constexpr int kUnit = 16 * NG * kWarps;       // cache rows of a unit
-    static constexpr int kStages = RB == 64 ? 4 : 2;
-    static constexpr int kGroup = 32 * RB;               // bytes of a group, k and v
-    static constexpr int kWarpStage = NG * kGroup;
-    static constexpr int kExpOff = kStages * kWarps * kWarpStage;  // 32 bytes a group
-    static constexpr int kMetaOff = kExpOff + kStages * kWarps * NG * 32;
+    static constexpr int kCtas = 2;
+    static constexpr int kUnit = 16 * NG * kWarps;   // cache rows of a unit
+    static constexpr int kHalf = 16 * RB;            // bytes of a group's keys, or values
+    static constexpr int kTurn = NG * 2 * kHalf;     // bytes of a warp's turn
+    static constexpr int kRoom = (220 / kCtas - 2) * 1024 / (kWarps * kTurn);
+    static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
+    static constexpr int kExpOff = kStages * kWarps * kTurn;  // 32 bytes a group
+    static constexpr int kBarOff = kExpOff + kStages * kWarps * NG * 32;
+    static constexpr int kMetaOff = kBarOff + kStages * kWarps * 8;
     static constexpr int kMlOff = kMetaOff + kStages * kWarps * 4;
-    static constexpr int kSmem = kMlOff + kWarps * NH * 8 * 8;
-    // a warp's outputs wait for the join in its part of the stage just read:
+    static constexpr int kNextOff = kMlOff + kWarps * NH * 8 * 8;  // next range, abort flag
+    static constexpr int kSmem = 1024 + kNextOff + 16;
+    static_assert(kStages >= 2, "queue");
+    // A warp's outputs wait for the join in its part of the turn just read:
     // [D][8] floats for each 8 heads, 8 more behind every 16 rows where there is
-    // room (bank conflicts)
-    static constexpr int kPad = (D + D / 16) * 8 * 4 * NH <= kWarpStage ? 8 : 0;
+    // room (bank conflicts).
+    static constexpr int kPad = (D + D / 16) * 8 * 4 * NH <= kTurn ? 8 : 0;
     static constexpr int kJoinHeads = (D * 8 + D / 16 * kPad);  // floats of 8 heads
-    static_assert(kJoinHeads * 4 * NH <= kWarpStage, "join buffer");
-};
-
-// Where a share stands: unit u of the U units of (sequence b, head block hh).
-template <int kUnit>
-struct Cursor {
-    int b, hh, u, U, len;
-    // On to the next unit; true where the item changed.
-    __device__ __forceinline__ bool next(const PagedArgs &p, int HH) {
-        if (++u < U) return false;
-        u = 0;
-        if (++hh < HH) return true;
-        hh = 0;
-        do {
-            if (++b >= p.n_seq) return true;
-            len = seq_len(p, b, false);
-            U = units_of<kUnit>(len);
-        } while (U == 0);
-        return true;
+    static_assert(kJoinHeads * 4 * NH <= kTurn, "join buffer");
+    // The cache row that column n of S's 8 stands for, and the byte in a box of
+    // 16-byte piece x of row r (TMA's swizzle of 128- and 64-byte rows).
+    static __device__ __forceinline__ int row_of(int n) {
+        return SB == 128 ? (n >> 1) + 4 * (n & 1) : n;
+    }
+    static __device__ __forceinline__ int piece(int r, int x) {
+        return r * SB + ((x ^ (SB == 128 ? r & 7 : (r >> 1) & 3)) << 4);
     }
 };
 
 template <int D, bool Q8, int NH>
-__global__ void __launch_bounds__(kThreads, 3)
-paged_attn_kernel(const PagedArgs p) {
+__global__ void __launch_bounds__(kThreads, Shape<D, Q8, NH>::kCtas)
+paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                  const PagedArgs p) {
     using S = Shape<D, Q8, NH>;
     constexpr int NG = S::NG;
-    constexpr int kSteps = D / 16;  // 16-wide steps along D of a score; 16-row tiles of O^T
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int kSteps = D / 16;  // 16-row tiles of O^T
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     griddep_launch_dependents();
-    griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int HH = p.H * p.HB;
-
-    // this CTA's share
-    const int total = units_before<S::kUnit>(p, p.n_seq) * HH;
-    const int ctas = min((int)gridDim.x, total);  // no share is empty
-    if ((int)blockIdx.x >= ctas) return;
-    const int u0 = share_begin(total, blockIdx.x, ctas);
-    const int u1 = share_begin(total, blockIdx.x + 1, ctas);
-    Cursor<S::kUnit> at;  // the unit to compute next
-    {
-        int b0 = 0, before = 0;  // (in units of one head)
-        while (true) {
-            const int i = b0 + lane;
-            const int U = i < p.n_seq
-                              ? units_of<S::kUnit>(seq_len(p, i, blockIdx.x == 0 && warp == 0))
-                              : 0;
-            int incl = U;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += o;
-            }
-            const bool beyond = (int64_t)(before + incl) * HH > u0;
-            const unsigned m = __ballot_sync(0xffffffffu, beyond);
-            if (m) {
-                const int l = __ffs(m) - 1;
-                at.b = b0 + l;
-                at.U = __shfl_sync(0xffffffffu, U, l);
-                const int rest = u0 - (before + __shfl_sync(0xffffffffu, incl - U, l)) * HH;
-                at.hh = rest / at.U;
-                at.u = rest % at.U;
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, incl, 31);
-            b0 += 32;
-        }
-        at.len = seq_len(p, at.b, false);
-    }
-
     const uint32_t base = smem_u32(smem);
-    int *meta = reinterpret_cast<int *>(smem + S::kMetaOff);
-    // ---- copies: `ahead` is the unit to copy next, `page` its pages (loaded one
-    // unit early), `kvh` its kv head
+    const uint32_t bars = base + S::kBarOff + warp * S::kStages * 8;
+    uint8_t *turns = smem + warp * S::kStages * S::kTurn;  // this warp's queue
+    uint8_t *exps = smem + S::kExpOff + warp * S::kStages * NG * 32;
+    int *meta = reinterpret_cast<int *>(smem + S::kMetaOff) + warp * S::kStages;
+    int *next_range = reinterpret_cast<int *>(smem + S::kNextOff);
+    volatile int *abort_flag = next_range + 1;
+    if (lane == 0) {
+        for (int s = 0; s < S::kStages; ++s) mbar_init(bars + 8 * s, 1);
+        fence_mbar_init();
+        if (warp == 0) {
+            tma_prefetch_desc(&mK);
+            tma_prefetch_desc(&mV);
+            *abort_flag = 0;
+        }
+    }
+    __syncthreads();
+    griddep_wait();
+    const int HH = p.H * p.HB;
+    const int total =
+        units_before<S::kUnit>(p, p.n_seq, blockIdx.x == 0 && warp == 0) * HH;
+    const Split split(total, p.ways, p.taken != nullptr);
+    if ((int)blockIdx.x >= split.ways || total == 0) return;
+    const WaitCtl wc{p.wait_ns, p.err, abort_flag, 0u};
+    bool ok = true;       // no wait of this warp has run out
+    int fills = 0;        // turns copied, and the place in the queue of the next
+    int put = 0, stage = 0;
+    uint32_t phase = 0;   // of the turn to read next, at `stage`
+
+    // ---- one range after another
+    for (int range = split.own(blockIdx.x);;) {
+    const int u0 = split.begin(range), u1 = split.begin(range + 1);
+    Cursor<S::kUnit> at = locate<S::kUnit>(p, HH, u0);  // the unit to compute next
+    // ---- copies, by lane 0: `ahead` is the unit to copy next, `page` its pages
+    // (loaded one unit early), `kvh_ahead` its kv head, `left` the units from it on
     Cursor<S::kUnit> ahead = at;
-    int left = u1 - u0;  // units not yet copied
+    int left = u1 - u0;
     int kvh_ahead = ahead.hh / p.HB;
     int page[NG];
     auto find_pages = [&]() {
@@ -258,125 +181,97 @@ paged_attn_kernel(const PagedArgs p) {
                 page[i] = __ldg(p.table + (int64_t)ahead.b * p.max_pages + (tok >> p.log2_page));
         }
     };
-    find_pages();
-    auto copy = [&](int stage) {
-        if (left > 0) {
-            int told = 0;
+    if (lane == 0) find_pages();
+    auto copy = [&]() {
+        if (lane == 0 && left > 0 && ok) {
+            const uint32_t bar = bars + 8 * put;
+            int rows[NG], told = 0, groups = 0;
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 const int tok = ahead.u * S::kUnit + (warp * NG + i) * 16;
-                int rows = min(max(ahead.len - tok, 0), 16);
+                rows[i] = min(max(ahead.len - tok, 0), 16);
                 if ((unsigned)page[i] >= (unsigned)p.n_pages) {
-                    if (rows && lane == 0) atomicOr(p.err, kDevErrAlign);
-                    rows = 0;
+                    if (rows[i]) atomicOr(p.err, kDevErrAlign);
+                    rows[i] = 0;
                 }
-                told |= rows << (8 * i);
-                const int64_t row = rows ? ((((int64_t)page[i] * p.H + kvh_ahead) << p.log2_page) +
-                                            (tok & ((1 << p.log2_page) - 1)))
-                                         : 0;
-                const uint32_t dst = base + (uint32_t)((stage * kWarps + warp) * S::kWarpStage +
-                                                       i * S::kGroup);
-                const uint32_t kd = dst + lane * 16, vd = dst + 2 * S::KC * 512 + lane * S::VB;
-                const uint8_t *kr = p.k + row * S::RB + g * S::RB + 16 * t;
-                const uint8_t *vr = p.v + row * S::RB + 2 * t * S::RB + g * S::VB;
-                if (rows == 16) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int c = 0; c < S::KC; ++c)
-                            cp_async<16>(kd + (j * S::KC + c) * 512, kr + 8 * j * S::RB + 64 * c);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int c = 0; c < S::VC; ++c)
-                            cp_async<S::VB>(vd + (j * S::VC + c) * (32 * S::VB),
-                                            vr + ((j & 1) + 8 * (j >> 1)) * S::RB + c * 8 * S::VB);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int c = 0; c < S::KC; ++c) {
-                            const bool in = 8 * j + g < rows;
-                            cp_async_part<16>(kd + (j * S::KC + c) * 512,
-                                              in ? kr + 8 * j * S::RB + 64 * c : p.k, in);
-                        }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int c = 0; c < S::VC; ++c) {
-                            const int r = (j & 1) + 8 * (j >> 1);
-                            const bool in = 2 * t + r < rows;
-                            cp_async_part<S::VB>(vd + (j * S::VC + c) * (32 * S::VB),
-                                                 in ? vr + r * S::RB + c * 8 * S::VB : p.v, in);
-                        }
-                }
-                if (Q8 && lane < 2)
-                    cp_async_part<16>(base + S::kExpOff +
-                                          ((stage * kWarps + warp) * NG + i) * 32 + lane * 16,
-                                      (lane ? p.v_exp : p.k_exp) + row, rows > 0);
+                told |= rows[i] << (8 * i);
+                groups += rows[i] > 0;
             }
-            if (lane == 0) meta[stage * kWarps + warp] = told;
+            meta[put] = told;
+            mbar_arrive_expect_tx(bar, groups * (2 * S::kHalf + (Q8 ? 32 : 0)));
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                if (rows[i] == 0) continue;
+                const int slot = (kvh_ahead << p.log2_page) +
+                                 ((ahead.u * S::kUnit + (warp * NG + i) * 16) &
+                                  ((1 << p.log2_page) - 1));
+                const uint32_t dst = smem_u32(turns) + put * S::kTurn + i * 2 * S::kHalf;
+#pragma unroll
+                for (int c = 0; c < S::NS; ++c) {
+                    tma_load_3d(dst + c * 16 * S::SB, &mK, bar, c * S::SB / 2, slot, page[i]);
+                    tma_load_3d(dst + S::kHalf + c * 16 * S::SB, &mV, bar, c * S::SB / 2, slot,
+                                page[i]);
+                }
+                if (Q8) {
+                    const int64_t row = (((int64_t)page[i] * p.H) << p.log2_page) + slot;
+                    const uint32_t ex = smem_u32(exps) + (put * NG + i) * 32;
+                    bulk_load(ex, p.k_exp + row, 16, bar);
+                    bulk_load(ex + 16, p.v_exp + row, 16, bar);
+                }
+            }
+            ++fills;
+            put = put + 1 == S::kStages ? 0 : put + 1;
             if (--left > 0) {
                 if (ahead.next(p, HH)) kvh_ahead = ahead.hh / p.HB;
                 find_pages();
             }
         }
-        cp_async_commit();  // (an empty group keeps the count)
     };
-#pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) copy(s);
+#pragma unroll 1
+    for (int s = 0; s < S::kStages - 1; ++s) copy();
 
     // ---- one item after another
-    int stage = 0;
     bool first = true;
     for (int u = u0; u < u1;) {
         const int units = min(at.U - at.u, u1 - u);  // of this item, in this share
         const bool whole = at.u == 0 && units == at.U;
         const int kvh = at.hh / p.HB, h0 = kvh * p.G + (at.hh % p.HB) * 8 * NH;
         const int heads = min(8 * NH, (kvh + 1) * p.G - h0);
-        // the queries as A operands: step s of piece c covers elements
-        // d = c * 64 / EB + t * 16 / EB + 4 s .. + 3 of heads g and g + 8
+        // the queries as A operands: word w of piece c goes with elements
+        // d = (64 c + 16 t) / EB + 4 w .. + 3 of heads g + 8 h
         uint32_t qa[kSteps][2][NH];
-        float qs[NH];  // what a score of head g + 8 i is multiplied by, in log2 units
+        float qs[NH];  // what a score of head g + 8 h is multiplied by, in log2 units
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-            const int h = g + 8 * i;
-            const __nv_bfloat16 *src = p.q + (int64_t)at.b * p.q_stride + (int64_t)(h0 + h) * D;
-            constexpr int kPer = 16 / S::EB;  // elements of a piece
-            uint32_t raw[kSteps][2];
+        for (int h = 0; h < NH; ++h) {
+            const __nv_bfloat16 *src =
+                p.q + (int64_t)at.b * p.q_stride + (int64_t)(h0 + g + 8 * h) * D;
+            uint2 raw[kSteps];
             uint32_t amax = 0;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                const int c = s / (kPer / 4), w = s % (kPer / 4);
-                uint2 x = make_uint2(0u, 0u);
-                if (h < heads)
-                    x = __ldg(reinterpret_cast<const uint2 *>(src + c * 4 * kPer + t * kPer + 4 * w));
-                raw[s][0] = x.x;
-                raw[s][1] = x.y;
-                if (Q8) {
-                    amax = max(amax, max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu));
-                    amax = max(amax, max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
-                }
+                constexpr int kPer = 16 / S::EB / 4;  // words of a piece
+                const int d = (64 * (s / kPer) + 16 * t) / S::EB + 4 * (s % kPer);
+                raw[s] = make_uint2(0u, 0u);
+                if (g + 8 * h < heads) raw[s] = __ldg(reinterpret_cast<const uint2 *>(src + d));
+                amax = max(amax, max(raw[s].x & 0x7fffu, (raw[s].x >> 16) & 0x7fffu));
+                amax = max(amax, max(raw[s].y & 0x7fffu, (raw[s].y >> 16) & 0x7fffu));
             }
-            qs[i] = p.scale_log2;
+            qs[h] = p.scale_log2;
+            float down = 1.f;
             if (Q8) {
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 // 2^(14 - exponent of the largest); both powers stay in fp32's range
                 const int ex = min(max((int)(amax >> 7), 15), 254) - 127 - 14;
-                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                qs[i] *= __uint_as_float((uint32_t)(127 + ex) << 23);
+                down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                qs[h] *= __uint_as_float((uint32_t)(127 + ex) << 23);
+            }
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-                        qa[s][w][i] = pack16<true>(nact_lo(raw[s][w]) * down,
-                                                   nact_hi(raw[s][w]) * down);
-            } else {
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) qa[s][w][i] = raw[s][w];
+            for (int s = 0; s < kSteps; ++s) {
+                qa[s][0][h] = Q8 ? pack16<true>(nact_lo(raw[s].x) * down, nact_hi(raw[s].x) * down)
+                                 : raw[s].x;
+                qa[s][1][h] = Q8 ? pack16<true>(nact_lo(raw[s].y) * down, nact_hi(raw[s].y) * down)
+                                 : raw[s].y;
             }
         }
         float m[NH], l[NH];  // of head g + 8 i; the sum over this thread's rows alone
@@ -392,12 +287,13 @@ paged_attn_kernel(const PagedArgs p) {
         }
 
         for (int n = 0; n < units; ++n) {
-            cp_async_wait<S::kStages - 2>();
-            __syncwarp();  // the other lanes' copies (exponents, meta) too; stage - 1 is read
-            copy(stage == 0 ? S::kStages - 1 : stage - 1);
-            const uint8_t *src = smem + (stage * kWarps + warp) * S::kWarpStage;
-            const int rows = meta[stage * kWarps + warp];
-            // S = Q K^T for rows 8 j + 2 t, + 1 of a group and heads g, g + 8
+            __syncwarp();  // the turn before this one is read: its place is free
+            copy();
+            ok = ok && mbar_wait_warp<false>(bars + 8 * stage, phase, wc);
+            if (!ok) continue;  // (on to the barriers of the join)
+            const uint8_t *src = turns + stage * S::kTurn;
+            const int rows = meta[stage];
+            // S = Q K^T: columns 2 t and 2 t + 1 of each 8 rows of a group, heads g, g + 8
             float sc[NG][2][4] = {};
 #pragma unroll
             for (int c = 0; c < S::KC; ++c) {
@@ -407,7 +303,8 @@ paged_attn_kernel(const PagedArgs p) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         w4[i][j] = *reinterpret_cast<const uint4 *>(
-                            src + i * S::kGroup + (j * S::KC + c) * 512 + lane * 16);
+                            src + i * 2 * S::kHalf + c * 64 / S::SB * 16 * S::SB +
+                            S::piece(8 * j + S::row_of(g), c * 4 % (S::SB / 16) + t));
                 constexpr int kPiece = Q8 ? 4 : 2;  // steps of a piece
 #pragma unroll
                 for (int k = 0; k < kPiece; ++k) {
@@ -425,25 +322,35 @@ paged_attn_kernel(const PagedArgs p) {
                         }
                 }
             }
-            // the rows' scales: keys' as factors, values' as exponents
+            // the rows' scales: keys' as factors, values' as exponents.  Column c of
+            // this thread's two is byte t of the 4 rows 4 c .. of 8 (rows of 128 bytes)
+            // or byte 2 t + c.
             float kf[NG][2][2], ve[NG][2][2];
 #pragma unroll
-            for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    kf[i][j][0] = kf[i][j][1] = 1.f;
-                    ve[i][j][0] = ve[i][j][1] = 0.f;
-                    if (!Q8) continue;
-                    const uint8_t *ex =
-                        smem + S::kExpOff + ((stage * kWarps + warp) * NG + i) * 32 + 8 * j + 2 * t;
-                    const uint32_t kx = *reinterpret_cast<const uint16_t *>(ex);
-                    const uint32_t vx = *reinterpret_cast<const uint16_t *>(ex + 16);
-                    kf[i][j][0] = __uint_as_float((kx << 23) & 0x7f800000u);
-                    kf[i][j][1] = __uint_as_float((kx << 15) & 0x7f800000u);
-                    // 2^23 + code, less 2^23 + 127
-                    ve[i][j][0] = __uint_as_float(__byte_perm(vx, 0x4b000000u, 0x7440)) - 8388735.f;
-                    ve[i][j][1] = __uint_as_float(__byte_perm(vx, 0x4b000000u, 0x7441)) - 8388735.f;
+            for (int i = 0; i < NG; ++i) {
+                uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
+                if (Q8) {
+                    kx = *reinterpret_cast<const uint4 *>(exps + (stage * NG + i) * 32);
+                    vx = *reinterpret_cast<const uint4 *>(exps + (stage * NG + i) * 32 + 16);
                 }
+                const uint32_t kw[4] = {kx.x, kx.y, kx.z, kx.w}, vw[4] = {vx.x, vx.y, vx.z, vx.w};
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        kf[i][j][c] = 1.f;
+                        ve[i][j][c] = 0.f;
+                        if (!Q8) continue;
+                        const uint32_t ka = S::SB == 128 ? kw[2 * j + c] : t < 2 ? kw[2 * j] : kw[2 * j + 1];
+                        const uint32_t va = S::SB == 128 ? vw[2 * j + c] : t < 2 ? vw[2 * j] : vw[2 * j + 1];
+                        const uint32_t at_byte = S::SB == 128 ? t : (2 * t + c) & 3;
+                        // the code to an exponent; 2^23 + code, less 2^23 + 127
+                        kf[i][j][c] =
+                            __uint_as_float(__byte_perm(ka, 0u, 0x0444u | (at_byte << 12)) >> 1);
+                        ve[i][j][c] = __uint_as_float(__byte_perm(va, 0x4b000000u, 0x7440u | at_byte)) -
+                                      8388735.f;
+                    }
+            }
             uint32_t pb[NH][NG][2];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
@@ -462,7 +369,7 @@ paged_attn_kernel(const PagedArgs p) {
                         for (int j = 0; j < 2; ++j)
 #pragma unroll
                             for (int c = 0; c < 2; ++c)
-                                if (8 * j + 2 * t + c >= ((rows >> (8 * i)) & 0xff))
+                                if (8 * j + S::row_of(2 * t + c) >= ((rows >> (8 * i)) & 0xff))
                                     s[i][j][c] = -INFINITY;
                 }
 #pragma unroll
@@ -510,13 +417,17 @@ paged_attn_kernel(const PagedArgs p) {
             // (rows g + 8) of this thread's piece of the value rows
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                const uint8_t *vsrc = src + i * S::kGroup + 2 * S::KC * 512 + lane * S::VB;
+                const uint8_t *vsrc = src + i * 2 * S::kHalf + S::kHalf;
+                const int have = (rows >> (8 * i)) & 0xff;
 #pragma unroll
                 for (int c = 0; c < S::VC; ++c) {
                     uint32_t r[4][S::VB / 4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint8_t *a = vsrc + (j * S::VC + c) * (32 * S::VB);
+                        const int row = S::row_of(2 * t + (j & 1)) + 8 * (j >> 1);
+                        const uint8_t *a = vsrc + c * 16 * S::SB +
+                                           S::piece(row, S::VB == 16 ? g : g >> 1) +
+                                           (S::VB == 16 ? 0 : (g & 1) * 8);
                         if (S::VB == 16) {
                             const uint4 x = *reinterpret_cast<const uint4 *>(a);
                             r[j][0] = x.x;
@@ -528,6 +439,13 @@ paged_attn_kernel(const PagedArgs p) {
                             r[j][0] = x.x;
                             r[j][1] = x.y;
                         }
+                    }
+                    if (have != 16) {  // what lies behind the length may be anything
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int x = 0; x < S::VB / 4; ++x)
+                                if (S::row_of(2 * t + (j & 1)) + 8 * (j >> 1) >= have) r[j][x] = 0u;
                     }
 #pragma unroll
                     for (int x = 0; x < S::VB / 4; ++x) {
@@ -564,13 +482,16 @@ paged_attn_kernel(const PagedArgs p) {
                     }
                 }
             }
-            stage = stage + 1 == S::kStages ? 0 : stage + 1;
+            if (++stage == S::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
 
         // ---- join the warps, then leave the result or a partial one.  A warp's
-        // outputs go to its part of the stage that it has just read (the next copy
-        // into it comes after the second barrier).
-        uint8_t *last = smem + (stage == 0 ? S::kStages - 1 : stage - 1) * kWarps * S::kWarpStage;
+        // outputs go to the turn that it has just read (the next copy into it comes
+        // after the second barrier).
+        const int last = (stage == 0 ? S::kStages : stage) - 1;
         float2 *ml = reinterpret_cast<float2 *>(smem + S::kMlOff);
         __syncwarp();
 #pragma unroll
@@ -578,7 +499,7 @@ paged_attn_kernel(const PagedArgs p) {
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             if (t == 0) ml[(warp * NH + i) * 8 + g] = make_float2(m[i], l[i]);
-            float *dst = reinterpret_cast<float *>(last + warp * S::kWarpStage) + i * S::kJoinHeads;
+            float *dst = reinterpret_cast<float *>(turns + last * S::kTurn) + i * S::kJoinHeads;
             constexpr int kEl = S::VB / S::EB;  // elements of a value piece
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
@@ -591,7 +512,7 @@ paged_attn_kernel(const PagedArgs p) {
             }
         }
         __syncthreads();
-        const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+        const int slot = 2 * range + (first ? 0 : 1);
         for (int e = threadIdx.x; e < heads * D; e += kThreads) {
             const int h = e / D, d = e % D;
             const int i = h >> 3, hr = h & 7;
@@ -606,7 +527,8 @@ paged_attn_kernel(const PagedArgs p) {
             for (int w = 0; w < kWarps; ++w) {
                 const float f = mw[w] == -INFINITY ? 0.f : exp2_fast(mw[w] - top);
                 sum += f * ml[(w * NH + i) * 8 + hr].y;
-                acc += f * reinterpret_cast<const float *>(last + w * S::kWarpStage)
+                acc += f * reinterpret_cast<const float *>(
+                               smem + (w * S::kStages + last) * S::kTurn)
                                [i * S::kJoinHeads + d * 8 + (d >> 4) * S::kPad + hr];
             }
             if (whole) {
@@ -617,80 +539,145 @@ paged_attn_kernel(const PagedArgs p) {
                 if (d == 0) p.part_ml[slot * (8 * NH) + h] = make_float2(top, sum);
             }
         }
-        __syncthreads();  // the join buffers are free for the next item
+        fence_proxy_async_smem();  // the buffers' next writer is the TMA
+        __syncthreads();           // and they are free for the next item
         first = false;
         // on to the next item of the share
         u += units;
         at.u += units - 1;
         if (u < u1) at.next(p, HH);
     }
-    cp_async_wait<0>();
+    if (!split.small) break;
+    if (threadIdx.x == 0) *next_range = split.taken(atomicAdd(p.taken, 1));
+    __syncthreads();
+    range = *next_range;
+    __syncthreads();  // (read before it is written again)
+    if (range >= split.ranges) break;
+    }
+    if (!ok && lane == 0) {
+        // Aborted: let every copy in flight land before shared memory goes away.
+        volatile int no_abort = 0;
+        const WaitCtl dc{kPagedDrainNs, p.err, &no_abort, kDevErrTimeout | kDevErrDrain};
+        for (int i = fills > S::kStages ? fills - S::kStages : 0; i < fills; ++i)
+            mbar_wait<false>(bars + 8 * (i % S::kStages), (uint32_t)(i / S::kStages) & 1u, dc);
+    }
 }
 
-// Joins the partial results of the items that were cut between CTAs, and
-// writes zeros for sequences without rows.  One block of D threads for each
-// (query head, sequence): the parts' weights side by side, then the sum of the
-// parts in their order.
-template <int D, int kUnit>
-__global__ void __launch_bounds__(D)
-paged_join_kernel(const PagedArgs p, int most_ctas, int block_heads) {
-    __shared__ float weight[kMaxCtas];
-    __shared__ float2 warp_ml[D / 32];
+// The counter of ranges taken, before the launch that counts them.
+__global__ void paged_begin_kernel(int *taken) {
     griddep_launch_dependents();
     griddep_wait();
-    const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
-    __nv_bfloat16 *out = p.out + (int64_t)b * p.out_stride + (int64_t)h * D + d;
+    *taken = 0;
+}
+
+// Joins the partial results of the items that were cut between ranges, and
+// writes zeros for sequences without rows.  One block for each (query head,
+// sequence): the parts' weights side by side, then a warp for every eighth part.
+template <int D, int kUnit>
+__global__ void __launch_bounds__(kJoinThreads)
+paged_join_kernel(const PagedArgs p, int block_heads) {
+    constexpr int kW = kJoinThreads / 32, E = D / 32;
+    __shared__ float weight[kMaxRanges];
+    __shared__ float2 warp_ml[kW];
+    __shared__ float acc_w[kW][D];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
+    __nv_bfloat16 *out = p.out + (int64_t)b * p.out_stride + (int64_t)h * D;
     const int U = units_of<kUnit>(seq_len(p, b, false));
     if (U == 0) {
-        *out = __float2bfloat16(0.f);
+        if (tid < D) out[tid] = __float2bfloat16(0.f);
         return;
     }
     const int HH = p.H * p.HB;
     const int kvh = h / p.G, hb = (h % p.G) / block_heads, hr = (h % p.G) % block_heads;
-    const int total = units_before<kUnit>(p, p.n_seq) * HH;
-    const int ctas = min(most_ctas, total);
-    const int i0 = units_before<kUnit>(p, b) * HH + (kvh * p.HB + hb) * U;
-    const int c0 = share_of(total, i0, ctas), c1 = share_of(total, i0 + U - 1, ctas);
-    if (c0 == c1) return;  // one CTA held the whole item and wrote it
-    // the item lies in the first slot of its CTAs, but for one that began before it
-    const int s0 = 2 * c0 + (share_begin(total, c0, ctas) < i0 ? 1 : 0);
-    auto slot_of = [&](int c) { return (c == c0 ? s0 : 2 * c) * block_heads + hr; };
+    const Split split(units_before<kUnit>(p, p.n_seq, false) * HH, p.ways, p.taken != nullptr);
+    const int i0 = units_before<kUnit>(p, b, false) * HH + (kvh * p.HB + hb) * U;
+    const int r0 = split.of(i0), n = split.of(i0 + U - 1) - r0 + 1;
+    if (n == 1) return;  // one range held the whole item: it is written
+    // the item lies in the first slot of its ranges, but for one that began before it
+    const int s0 = 2 * r0 + (split.begin(r0) < i0 ? 1 : 0);
+    auto slot_of = [&](int i) { return (i == 0 ? s0 : 2 * (r0 + i)) * block_heads + hr; };
     float top = -INFINITY;
-    for (int c = c0 + d; c <= c1; c += D) top = fmaxf(top, p.part_ml[slot_of(c)].x);
+    for (int i = tid; i < n; i += kJoinThreads) top = fmaxf(top, p.part_ml[slot_of(i)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if ((d & 31) == 0) warp_ml[d >> 5].x = top;
+    if (lane == 0) warp_ml[warp].x = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) top = fmaxf(top, warp_ml[w].x);
+    for (int w = 0; w < kW; ++w) top = fmaxf(top, warp_ml[w].x);
     float sum = 0.f;
-    for (int c = c0 + d; c <= c1; c += D) {
-        const float2 ml = p.part_ml[slot_of(c)];
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const float2 ml = p.part_ml[slot_of(i)];
         const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
-        weight[c - c0] = f;
+        weight[i] = f;
         sum += f * ml.y;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if ((d & 31) == 0) warp_ml[d >> 5].y = sum;
+    if (lane == 0) warp_ml[warp].y = sum;
     __syncthreads();
-    sum = 0.f;
+    float acc[E] = {};
+    constexpr int kBatch = 8;  // loads in flight
+    for (int at = warp; at < n; at += kW * kBatch) {
+        float2 x[kBatch][E / 2];
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) sum += warp_ml[w].y;
-    float acc = weight[0] * p.part_o[(int64_t)slot_of(c0) * D + d];
-#pragma unroll 8
-    for (int c = c0 + 1; c <= c1; ++c) acc += weight[c - c0] * p.part_o[(int64_t)slot_of(c) * D + d];
-    *out = __float2bfloat16(sum > 0.f || sum != sum ? acc / sum : 0.f);
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = at + k * kW;
+            const float *src = p.part_o + (int64_t)slot_of(min(i, n - 1)) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) x[k][e] = reinterpret_cast<const float2 *>(src)[e];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float f = at + k * kW < n ? weight[at + k * kW] : 0.f;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                acc[2 * e] = fmaf(f, x[k][e].x, acc[2 * e]);
+                acc[2 * e + 1] = fmaf(f, x[k][e].y, acc[2 * e + 1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc_w[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (tid < D) {
+        float a = 0.f;
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            a += acc_w[w][tid];
+            sum += warp_ml[w].y;
+        }
+        out[tid] = __float2bfloat16(sum > 0.f || sum != sum ? a / sum : 0.f);
+    }
 }
 
 int head_block(int G) { return G <= 8 ? 8 : 16; }
 
+// Whether a cache's rows go to the tcgen05 kernel: 8-bit rows of 128 elements, where
+// the tensor core takes the elements as they are (see paged_attn_tc.cu).
+bool on_tc(int D, bool e4m3) { return e4m3 && D == 128; }
+
+template <int D, int kUnit>
+cudaError_t launch_join(const PagedArgs &a, int block_heads, const LaunchCtx &ctx) {
+    return launch_pdl(paged_join_kernel<D, kUnit>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
+                      dim3(kJoinThreads), 0, ctx, a, block_heads);
+}
+
 template <int D, bool Q8, int NH>
-cudaError_t launch(const PagedArgs &a, const LaunchCtx &ctx) {
+cudaError_t launch(PagedArgs a, const KvCacheSpec &cache, const LaunchCtx &ctx) {
     using S = Shape<D, Q8, NH>;
-    const int64_t most_units =
-        (((int64_t)a.max_pages << a.log2_page) + S::kUnit - 1) / S::kUnit * a.n_seq * a.H * a.HB;
-    if (most_units > INT32_MAX) return cudaErrorInvalidValue;
+    // the cache as (bytes of a row, in pairs; rows of a page; pages), 16 rows a box
+    CUtensorMap mK, mV;
+    const cuuint64_t rows = (cuuint64_t)cache.H << cache.log2_page;
+    const cuuint64_t dims[3] = {S::RB / 2, rows, (cuuint64_t)cache.n_pages};
+    const cuuint64_t strides[2] = {S::RB, rows * S::RB};
+    const cuuint32_t box[3] = {S::SB / 2, 16, 1};
+    if (!encode_tiled_bf16(&mK, 3, cache.k, dims, strides, box, S::SB) ||
+        !encode_tiled_bf16(&mV, 3, cache.v, dims, strides, box, S::SB))
+        return cudaErrorInvalidValue;
     auto *kern = paged_attn_kernel<D, Q8, NH>;
     // resident CTAs, and the shared-memory opt-in, once per device
     constexpr int kMaxDev = 64;
@@ -708,19 +695,37 @@ cudaError_t launch(const PagedArgs &a, const LaunchCtx &ctx) {
         if (occ < 1) return cudaErrorInvalidConfiguration;
         per_sm[dev].store(occ, std::memory_order_release);
     }
-    const int ctas = (int)std::max<int64_t>(
-        1, std::min<int64_t>(most_units, std::min(kMaxCtas, occ * ctx.num_sms)));
-    e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), S::kSmem, ctx, a);
+    const bool takes = paged_ways(a, S::kUnit, std::min(kMaxWays, occ * ctx.num_sms));
+    count_launches(takes ? 3 : 2);
+    if (takes) {
+        e = launch_paged_begin(a, ctx);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(kern, dim3((unsigned)a.ways), dim3(kThreads), S::kSmem, ctx, mK, mV, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_join_kernel<D, S::kUnit>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
-                      dim3(D), 0, ctx, a, ctas, 8 * NH);
+    return launch_join<D, S::kUnit>(a, 8 * NH, ctx);
 }
 
 }  // namespace
 
+bool paged_ways(PagedArgs &a, int unit, int most) {
+    const int64_t rows = (int64_t)a.max_pages << a.log2_page;
+    const int64_t units = (rows + unit - 1) / unit * a.n_seq * a.H * a.HB;
+    a.ways = (int)std::max<int64_t>(1, std::min<int64_t>(units, most));
+    // pieces are taken where shares may have the units to cut them from
+    const bool takes = units >= 16 * (int64_t)a.ways;
+    if (!takes) a.taken = nullptr;
+    return takes;
+}
+
+cudaError_t launch_paged_begin(const PagedArgs &a, const LaunchCtx &ctx) {
+    return launch_pdl(paged_begin_kernel, dim3(1), dim3(1), 0, ctx, a.taken);
+}
+
+// The counter (256 bytes), then the parts' maxima and sums, then their outputs.
 size_t paged_attention_workspace(int Hq, int Hkv, int D) {
-    const size_t rows = (size_t)2 * kMaxCtas * head_block(Hq / Hkv);
-    return rows * (D * sizeof(float) + sizeof(float2));
+    const size_t rows = (size_t)2 * kMaxRanges * head_block(Hq / Hkv);
+    return 256 + rows * (D * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t q_stride,
@@ -730,8 +735,6 @@ cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t 
     PagedArgs a;
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.q_stride = q_stride;
-    a.k = static_cast<const uint8_t *>(c.k);
-    a.v = static_cast<const uint8_t *>(c.v);
     a.k_exp = c.k_exp;
     a.v_exp = c.v_exp;
     a.n_pages = c.n_pages;
@@ -747,19 +750,24 @@ cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t 
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.out_stride = out_stride;
-    const size_t rows = (size_t)2 * kMaxCtas * hb;
-    a.part_ml = static_cast<float2 *>(workspace);
+    const size_t rows = (size_t)2 * kMaxRanges * hb;
+    a.ways = 0;
+    a.taken = static_cast<int *>(workspace);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + 256);
     a.part_o = reinterpret_cast<float *>(a.part_ml + rows);
     a.err = ctx.err;
+    a.wait_ns = ctx.wait_ns;
+    if (on_tc(c.D, c.e4m3)) {
+        int heads = 0;
+        const cudaError_t e = launch_paged_tc(a, c, ctx, &heads);
+        return e != cudaSuccess ? e : launch_join<128, kPagedTcUnit>(a, heads, ctx);
+    }
     if (c.D == 64) {
-        if (c.e4m3) return hb == 8 ? launch<64, true, 1>(a, ctx) : launch<64, true, 2>(a, ctx);
-        return hb == 8 ? launch<64, false, 1>(a, ctx) : launch<64, false, 2>(a, ctx);
+        if (c.e4m3) return hb == 8 ? launch<64, true, 1>(a, c, ctx) : launch<64, true, 2>(a, c, ctx);
+        return hb == 8 ? launch<64, false, 1>(a, c, ctx) : launch<64, false, 2>(a, c, ctx);
     }
-    if (c.D == 128) {
-        if (c.e4m3)
-            return hb == 8 ? launch<128, true, 1>(a, ctx) : launch<128, true, 2>(a, ctx);
-        return hb == 8 ? launch<128, false, 1>(a, ctx) : launch<128, false, 2>(a, ctx);
-    }
+    if (c.D == 128)
+        return hb == 8 ? launch<128, false, 1>(a, c, ctx) : launch<128, false, 2>(a, c, ctx);
     return cudaErrorInvalidValue;
 }
 

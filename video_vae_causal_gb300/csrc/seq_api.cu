@@ -213,8 +213,8 @@ wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
     if (!(scale > 0.f) || !(scale < INFINITY)) return WANVAE_ERR_INVALID_ARG;
     const size_t need = wanvae_paged_attention_workspace_size(n_heads, s.H, s.D);
     if (need == 0) return WANVAE_ERR_UNSUPPORTED;
-    // the units of 64 rows that the page table could hold are counted in 32 bits
-    const int64_t units = ((max_pages << s.log2_page) + 63) / 64;
+    // the units of 16 rows that the page table could hold are counted in 32 bits
+    const int64_t units = ((max_pages << s.log2_page) + 15) / 16;
     if (units > INT32_MAX / 64 || units * n_seq > INT32_MAX / n_heads) return WANVAE_ERR_UNSUPPORTED;
     const int64_t w = n_heads * s.D;
     if (!stride_ok(q_stride, w) || !stride_ok(out_stride, w)) return WANVAE_ERR_INVALID_ARG;
@@ -228,7 +228,6 @@ wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
         return WANVAE_ERR_INVALID_ARG;
     LaunchCtx ctx;
     if (!make_launch_ctx(ctx, stream)) return WANVAE_ERR_CUDA;
-    count_launches(2);
     return from_cuda(launch_paged_attention(s, q, q_stride, lens, page_table, (int)max_pages,
                                             (int)n_seq, (int)n_heads, scale, out, out_stride,
                                             workspace, ctx));
