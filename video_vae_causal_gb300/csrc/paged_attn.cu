@@ -8,15 +8,15 @@
 // byte or less and the bound is HBM.
 //
 // Split.  The rows of one (sequence, kv head) are cut into units of 64 or 128; the
-// units of the whole batch, laid end to end, are dealt to the CTAs in contiguous
-// ranges: an equal share each, so a ragged batch and a single long sequence load
-// every multiprocessor alike, and of large batches the last tenth of each share apart,
-// for the CTA that is done first (multiprocessors differ by a tenth in the
-// bandwidth that they get).  A range may begin or end inside an item: then its
-// CTA leaves a partial result (the running maximum, the sum and the unnormalised
-// output) in the workspace, two slots a range, and a second small kernel joins them
-// in the ranges' order.  The ranges follow from the lengths alone, so neither
-// which CTA took one nor the order in which they end changes a bit.
+// units of the whole batch, laid end to end, are dealt to the CTAs in equal
+// contiguous shares, so a ragged batch and a single long sequence load every
+// multiprocessor alike.  A share may begin or end inside an item: then its CTA
+// leaves a partial result (the running maximum, the sum and the unnormalised output) in
+// the workspace, two slots a CTA, and a second small kernel joins them in the order of
+// the CTAs.  Which CTA left what follows from the lengths alone, so nothing is
+// counted, reset or raced for.  (Shares whose last tenth any CTA could take, by a
+// counter, ended within 5 % of each other instead of 10, but each piece so taken cost
+// its CTA 4 us to begin: 61 -> 67 us for 131040 rows of 8 heads.)
 //
 // A warp takes 16 or 32 rows of a unit, for which one lane starts two TMA loads of
 // 16 rows each (keys, values) into the warp's own queue, kStages turns deep; no
@@ -52,7 +52,7 @@ namespace wanvae {
 namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 
 // D += A B, 16 x 8 x 16, fp16 or bf16 in, fp32 out.
 template <bool F16>
@@ -93,6 +93,7 @@ struct Shape {
     static constexpr int NG = RB >= 256 ? 1 : 2;
     static constexpr int kCtas = 2;
     static constexpr int kUnit = 16 * NG * kWarps;   // cache rows of a unit
+    using U = Units<kUnit, 0>;
     static constexpr int kHalf = 16 * RB;            // bytes of a group's keys, or values
     static constexpr int kTurn = NG * 2 * kHalf;     // bytes of a warp's turn
     static constexpr int kRoom = (220 / kCtas - 2) * 1024 / (kWarps * kTurn);
@@ -101,8 +102,8 @@ struct Shape {
     static constexpr int kBarOff = kExpOff + kStages * kWarps * NG * 32;
     static constexpr int kMetaOff = kBarOff + kStages * kWarps * 8;
     static constexpr int kMlOff = kMetaOff + kStages * kWarps * 4;
-    static constexpr int kNextOff = kMlOff + kWarps * NH * 8 * 8;  // next range, abort flag
-    static constexpr int kSmem = 1024 + kNextOff + 16;
+    static constexpr int kAbortOff = kMlOff + kWarps * NH * 8 * 8;
+    static constexpr int kSmem = 1024 + kAbortOff + 16;
     static_assert(kStages >= 2, "queue");
     // A warp's outputs wait for the join in its part of the turn just read:
     // [D][8] floats for each 8 heads, 8 more behind every 16 rows where there is
@@ -138,8 +139,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
     uint8_t *turns = smem + warp * S::kStages * S::kTurn;  // this warp's queue
     uint8_t *exps = smem + S::kExpOff + warp * S::kStages * NG * 32;
     int *meta = reinterpret_cast<int *>(smem + S::kMetaOff) + warp * S::kStages;
-    int *next_range = reinterpret_cast<int *>(smem + S::kNextOff);
-    volatile int *abort_flag = next_range + 1;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbortOff);
     if (lane == 0) {
         for (int s = 0; s < S::kStages; ++s) mbar_init(bars + 8 * s, 1);
         fence_mbar_init();
@@ -152,9 +152,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
     __syncthreads();
     griddep_wait();
     const int HH = p.H * p.HB;
-    const int total =
-        units_before<S::kUnit>(p, p.n_seq, blockIdx.x == 0 && warp == 0) * HH;
-    const Split split(total, p.ways, p.taken != nullptr);
+    const int total = S::U::before(p, p.n_seq, blockIdx.x == 0 && warp == 0) * HH;
+    const Split split(total, p.ways);
     if ((int)blockIdx.x >= split.ways || total == 0) return;
     const WaitCtl wc{p.wait_ns, p.err, abort_flag, 0u};
     bool ok = true;       // no wait of this warp has run out
@@ -162,14 +161,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
     int put = 0, stage = 0;
     uint32_t phase = 0;   // of the turn to read next, at `stage`
 
-    // ---- one range after another
-    for (int range = split.own(blockIdx.x);;) {
-    const int u0 = split.begin(range), u1 = split.begin(range + 1);
-    Cursor<S::kUnit> at = locate<S::kUnit>(p, HH, u0);  // the unit to compute next
+    const int begin = split.begin(blockIdx.x);
+    Cursor<typename S::U> at =  // the unit to compute next
+        locate<typename S::U>(p, HH, begin, split.begin(blockIdx.x + 1) - begin);
     // ---- copies, by lane 0: `ahead` is the unit to copy next, `page` its pages
-    // (loaded one unit early), `kvh_ahead` its kv head, `left` the units from it on
-    Cursor<S::kUnit> ahead = at;
-    int left = u1 - u0;
+    // (loaded one unit early), `kvh_ahead` its kv head
+    Cursor<typename S::U> ahead = at;
     int kvh_ahead = ahead.hh / p.HB;
     int page[NG];
     auto find_pages = [&]() {
@@ -183,7 +180,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
     };
     if (lane == 0) find_pages();
     auto copy = [&]() {
-        if (lane == 0 && left > 0 && ok) {
+        if (lane == 0 && ahead.left > 0 && ok) {
             const uint32_t bar = bars + 8 * put;
             int rows[NG], told = 0, groups = 0;
 #pragma unroll
@@ -221,10 +218,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
             }
             ++fills;
             put = put + 1 == S::kStages ? 0 : put + 1;
-            if (--left > 0) {
-                if (ahead.next(p, HH)) kvh_ahead = ahead.hh / p.HB;
-                find_pages();
-            }
+            if (ahead.next(p, HH, 1)) kvh_ahead = ahead.hh / p.HB;
+            if (ahead.left > 0) find_pages();
         }
     };
 #pragma unroll 1
@@ -232,8 +227,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
 
     // ---- one item after another
     bool first = true;
-    for (int u = u0; u < u1;) {
-        const int units = min(at.U - at.u, u1 - u);  // of this item, in this share
+    while (at.left > 0) {
+        const int units = at.units();  // of this item, in this share
         const bool whole = at.u == 0 && units == at.U;
         const int kvh = at.hh / p.HB, h0 = kvh * p.G + (at.hh % p.HB) * 8 * NH;
         const int heads = min(8 * NH, (kvh + 1) * p.G - h0);
@@ -512,7 +507,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
             }
         }
         __syncthreads();
-        const int slot = 2 * range + (first ? 0 : 1);
+        const int slot = 2 * blockIdx.x + (first ? 0 : 1);
         for (int e = threadIdx.x; e < heads * D; e += kThreads) {
             const int h = e / D, d = e % D;
             const int i = h >> 3, hr = h & 7;
@@ -542,17 +537,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
         fence_proxy_async_smem();  // the buffers' next writer is the TMA
         __syncthreads();           // and they are free for the next item
         first = false;
-        // on to the next item of the share
-        u += units;
-        at.u += units - 1;
-        if (u < u1) at.next(p, HH);
-    }
-    if (!split.small) break;
-    if (threadIdx.x == 0) *next_range = split.taken(atomicAdd(p.taken, 1));
-    __syncthreads();
-    range = *next_range;
-    __syncthreads();  // (read before it is written again)
-    if (range >= split.ranges) break;
+        at.next(p, HH, units);  // on to the next item of the share
     }
     if (!ok && lane == 0) {
         // Aborted: let every copy in flight land before shared memory goes away.
@@ -563,21 +548,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
     }
 }
 
-// The counter of ranges taken, before the launch that counts them.
-__global__ void paged_begin_kernel(int *taken) {
-    griddep_launch_dependents();
-    griddep_wait();
-    *taken = 0;
-}
-
-// Joins the partial results of the items that were cut between ranges, and
+// Joins the partial results of the items that were cut between CTAs, and
 // writes zeros for sequences without rows.  One block for each (query head,
-// sequence): the parts' weights side by side, then a warp for every eighth part.
-template <int D, int kUnit>
+// sequence): the parts' weights side by side, then a warp for every fourth part.
+template <int D, class U>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const PagedArgs p, int block_heads) {
     constexpr int kW = kJoinThreads / 32, E = D / 32;
-    __shared__ float weight[kMaxRanges];
+    __shared__ float weight[kMaxWays];
     __shared__ float2 warp_ml[kW];
     __shared__ float acc_w[kW][D];
     griddep_launch_dependents();
@@ -585,20 +563,21 @@ paged_join_kernel(const PagedArgs p, int block_heads) {
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5;
     __nv_bfloat16 *out = p.out + (int64_t)b * p.out_stride + (int64_t)h * D;
-    const int U = units_of<kUnit>(seq_len(p, b, false));
-    if (U == 0) {
+    const int units = U::of(seq_len(p, b, false));
+    if (units == 0) {
         if (tid < D) out[tid] = __float2bfloat16(0.f);
         return;
     }
     const int HH = p.H * p.HB;
     const int kvh = h / p.G, hb = (h % p.G) / block_heads, hr = (h % p.G) % block_heads;
-    const Split split(units_before<kUnit>(p, p.n_seq, false) * HH, p.ways, p.taken != nullptr);
-    const int i0 = units_before<kUnit>(p, b, false) * HH + (kvh * p.HB + hb) * U;
-    const int r0 = split.of(i0), n = split.of(i0 + U - 1) - r0 + 1;
-    if (n == 1) return;  // one range held the whole item: it is written
-    // the item lies in the first slot of its ranges, but for one that began before it
-    const int s0 = 2 * r0 + (split.begin(r0) < i0 ? 1 : 0);
-    auto slot_of = [&](int i) { return (i == 0 ? s0 : 2 * (r0 + i)) * block_heads + hr; };
+    const Split split(U::before(p, p.n_seq, false) * HH, p.ways);
+    // the item's first place; its units are the last of its places
+    const int i0 = U::before(p, b, false) * HH + (kvh * p.HB + hb) * (units + U::kExtra);
+    const int w0 = split.of(i0 + U::kExtra), n = split.of(i0 + U::kExtra + units - 1) - w0 + 1;
+    if (n == 1) return;  // one CTA held the whole item: it is written
+    // the item lies in the first slot of its CTAs, but for one with units before it
+    const int s0 = 2 * w0 + (split.begin(w0) < i0 ? 1 : 0);
+    auto slot_of = [&](int i) { return (i == 0 ? s0 : 2 * (w0 + i)) * block_heads + hr; };
     float top = -INFINITY;
     for (int i = tid; i < n; i += kJoinThreads) top = fmaxf(top, p.part_ml[slot_of(i)].x);
 #pragma unroll
@@ -660,9 +639,10 @@ int head_block(int G) { return G <= 8 ? 8 : 16; }
 // the tensor core takes the elements as they are (see paged_attn_tc.cu).
 bool on_tc(int D, bool e4m3) { return e4m3 && D == 128; }
 
-template <int D, int kUnit>
+template <int D, class U>
 cudaError_t launch_join(const PagedArgs &a, int block_heads, const LaunchCtx &ctx) {
-    return launch_pdl(paged_join_kernel<D, kUnit>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
+    count_launches(1);
+    return launch_pdl(paged_join_kernel<D, U>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
                       dim3(kJoinThreads), 0, ctx, a, block_heads);
 }
 
@@ -695,37 +675,25 @@ cudaError_t launch(PagedArgs a, const KvCacheSpec &cache, const LaunchCtx &ctx) 
         if (occ < 1) return cudaErrorInvalidConfiguration;
         per_sm[dev].store(occ, std::memory_order_release);
     }
-    const bool takes = paged_ways(a, S::kUnit, std::min(kMaxWays, occ * ctx.num_sms));
-    count_launches(takes ? 3 : 2);
-    if (takes) {
-        e = launch_paged_begin(a, ctx);
-        if (e != cudaSuccess) return e;
-    }
+    a.ways = paged_ways(a, S::kUnit, std::min(kMaxWays, occ * ctx.num_sms));
+    count_launches(1);
     e = launch_pdl(kern, dim3((unsigned)a.ways), dim3(kThreads), S::kSmem, ctx, mK, mV, a);
     if (e != cudaSuccess) return e;
-    return launch_join<D, S::kUnit>(a, 8 * NH, ctx);
+    return launch_join<D, typename S::U>(a, 8 * NH, ctx);
 }
 
 }  // namespace
 
-bool paged_ways(PagedArgs &a, int unit, int most) {
-    const int64_t rows = (int64_t)a.max_pages << a.log2_page;
-    const int64_t units = (rows + unit - 1) / unit * a.n_seq * a.H * a.HB;
-    a.ways = (int)std::max<int64_t>(1, std::min<int64_t>(units, most));
-    // pieces are taken where shares may have the units to cut them from
-    const bool takes = units >= 16 * (int64_t)a.ways;
-    if (!takes) a.taken = nullptr;
-    return takes;
+int paged_ways(const PagedArgs &a, int rows, int most) {
+    const int64_t len = (int64_t)a.max_pages << a.log2_page;
+    const int64_t units = (len + rows - 1) / rows * a.n_seq * a.H * a.HB;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(units, most));
 }
 
-cudaError_t launch_paged_begin(const PagedArgs &a, const LaunchCtx &ctx) {
-    return launch_pdl(paged_begin_kernel, dim3(1), dim3(1), 0, ctx, a.taken);
-}
-
-// The counter (256 bytes), then the parts' maxima and sums, then their outputs.
+// The parts' maxima and sums, then their outputs.
 size_t paged_attention_workspace(int Hq, int Hkv, int D) {
-    const size_t rows = (size_t)2 * kMaxRanges * head_block(Hq / Hkv);
-    return 256 + rows * (D * sizeof(float) + sizeof(float2));
+    const size_t rows = (size_t)2 * kMaxWays * head_block(Hq / Hkv);
+    return rows * (D * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t q_stride,
@@ -750,17 +718,16 @@ cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t 
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.out_stride = out_stride;
-    const size_t rows = (size_t)2 * kMaxRanges * hb;
+    const size_t rows = (size_t)2 * kMaxWays * hb;
     a.ways = 0;
-    a.taken = static_cast<int *>(workspace);
-    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + 256);
+    a.part_ml = static_cast<float2 *>(workspace);
     a.part_o = reinterpret_cast<float *>(a.part_ml + rows);
     a.err = ctx.err;
     a.wait_ns = ctx.wait_ns;
     if (on_tc(c.D, c.e4m3)) {
         int heads = 0;
         const cudaError_t e = launch_paged_tc(a, c, ctx, &heads);
-        return e != cudaSuccess ? e : launch_join<128, kPagedTcUnit>(a, heads, ctx);
+        return e != cudaSuccess ? e : launch_join<128, TcUnits>(a, heads, ctx);
     }
     if (c.D == 64) {
         if (c.e4m3) return hb == 8 ? launch<64, true, 1>(a, c, ctx) : launch<64, true, 2>(a, c, ctx);

@@ -14,8 +14,6 @@
 namespace wanvae {
 
 constexpr int kMaxWays = 152 * 2;  // CTAs of a launch
-constexpr int kPieces = 2;         // ranges of a share that any CTA may take
-constexpr int kMaxRanges = (1 + kPieces) * kMaxWays;
 constexpr uint64_t kPagedDrainNs = 200ull * 1000 * 1000;
 
 struct PagedArgs {
@@ -30,9 +28,8 @@ struct PagedArgs {
     __nv_bfloat16 *out;
     int64_t out_stride;
     int ways;        // CTAs
-    int *taken;      // ranges taken beyond the shares; NULL: shares alone
-    float *part_o;   // [2 ranges][heads of a block][D]
-    float2 *part_ml; // [2 ranges][heads of a block]: maximum, sum
+    float *part_o;   // [2 CTAs][heads of a block][D]
+    float2 *part_ml; // [2 CTAs][heads of a block]: maximum, sum
     unsigned *err;
     uint64_t wait_ns;
 };
@@ -45,50 +42,37 @@ __device__ __forceinline__ int seq_len(const PagedArgs &p, int b, bool tell) {
     if (tell) atomicOr(p.err, kDevErrAlign);
     return len < 0 ? 0 : (int)most;
 }
-template <int kUnit>
-__device__ __forceinline__ int units_of(int len) {
-    return (len + kUnit - 1) / kUnit;
-}
 
-// Units before sequence b (all of them for b = n_seq) of one head; whole warp.
-template <int kUnit>
-__device__ __forceinline__ int units_before(const PagedArgs &p, int b, bool tell) {
-    const int lane = threadIdx.x & 31;
-    int n = 0;
-    for (int i = lane; i < b; i += 32) n += units_of<kUnit>(seq_len(p, i, tell));
-    return __reduce_add_sync(0xffffffffu, n);
-}
+// A kernel's units: kRows cached rows of one kv head, and what an item (a sequence
+// and a block of heads) costs besides them, in units.  Shares are cut in these,
+// places: an item of U units has kExtra + U, its units the last ones.
+template <int kRows_, int kExtra_>
+struct Units {
+    static constexpr int kRows = kRows_, kExtra = kExtra_;
+    static __device__ __forceinline__ int of(int len) { return (len + kRows - 1) / kRows; }
+    static __device__ __forceinline__ int places(int len) {
+        return len > 0 ? of(len) + kExtra : 0;
+    }
+    // Places before sequence b (all of them for b = n_seq) of one head; whole warp.
+    static __device__ __forceinline__ int before(const PagedArgs &p, int b, bool tell) {
+        int n = 0;
+        for (int i = threadIdx.x & 31; i < b; i += 32) n += places(seq_len(p, i, tell));
+        return __reduce_add_sync(0xffffffffu, n);
+    }
+};
 
-// How `total` units are cut: one share for each of `ways` CTAs, in order.  Where
-// ranges are taken, a share ends in kPieces pieces of `small` units, each a range
-// of its own, and what is left of it is its first range.
+// How `total` places are cut: one share for each of `ways` CTAs, in order.
 struct Split {
-    static constexpr int kOf = 1 + kPieces;  // ranges of a share
-    int ways, ranges, q, rem, small;
-    __device__ __forceinline__ Split(int total, int most, bool takes) {
+    int ways, q, rem;
+    __device__ __forceinline__ Split(int total, int most) {
         ways = max(1, min(most, total));  // (no share is empty)
         q = total / ways;
         rem = total - q * ways;
-        small = takes ? q / 16 : 0;
-        ranges = small ? kOf * ways : ways;
     }
-    __device__ __forceinline__ int share(int w) const { return q * w + min(w, rem); }
-    // The first range of CTA w, and the range taken as number n (first pieces first).
-    __device__ __forceinline__ int own(int w) const { return small ? kOf * w : w; }
-    __device__ __forceinline__ int taken(int n) const {
-        return n < kPieces * ways ? kOf * (n % ways) + 1 + n / ways : ranges;
-    }
-    __device__ __forceinline__ int begin(int r) const {
-        if (!small) return share(r);
-        const int w = r / kOf, j = r - w * kOf;
-        return j ? share(w + 1) - small * (kOf - j) : share(w);
-    }
-    __device__ __forceinline__ int of(int unit) const {  // (q is at least 1)
+    __device__ __forceinline__ int begin(int w) const { return q * w + min(w, rem); }
+    __device__ __forceinline__ int of(int place) const {  // (q is at least 1)
         const int big = rem * (q + 1);
-        const int w = unit < big ? unit / (q + 1) : rem + (unit - big) / q;
-        if (!small) return w;
-        const int behind = unit - (share(w + 1) - small * kPieces);
-        return kOf * w + (behind < 0 ? 0 : 1 + behind / small);
+        return place < big ? place / (q + 1) : rem + (place - big) / q;
     }
 };
 
@@ -102,50 +86,64 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
-// Where a range stands: unit u of the U units of (sequence b, head block hh).
-template <int kUnit>
+// Where a share stands: unit u of the U units of (sequence b, head block hh), `left`
+// places of the share from it on.
+template <class U_>
 struct Cursor {
-    int b, hh, u, U, len;
-    // On to the next unit; true where the item changed.
-    __device__ __forceinline__ bool next(const PagedArgs &p, int HH) {
-        if (++u < U) return false;
+    int b, hh, u, U, len, left;
+    // The item's units from here on that the share holds.
+    __device__ __forceinline__ int units() const { return min(U - u, left); }
+    // On to unit u + n of the item (n at most units()), or to the next item's first;
+    // true where the item changed.  The share has ended where left is 0.
+    __device__ __forceinline__ bool next(const PagedArgs &p, int HH, int n) {
+        u += n;
+        left -= n;
+        if (u < U) return false;
         u = 0;
-        if (++hh < HH) return true;
+        left = max(left - U_::kExtra, 0);
+        if (left == 0 || ++hh < HH) return true;
         hh = 0;
         do {
-            if (++b >= p.n_seq) return true;
+            if (++b >= p.n_seq) {
+                left = 0;
+                return true;
+            }
             len = seq_len(p, b, false);
-            U = units_of<kUnit>(len);
+            U = U_::of(len);
         } while (U == 0);
         return true;
     }
 };
 
-// The cursor of a unit of the whole batch (whole warp).
-template <int kUnit>
-__device__ __forceinline__ Cursor<kUnit> locate(const PagedArgs &p, int HH, int unit) {
+// The first unit of a share that begins at `place` of the batch and has `left`
+// places (whole warp).
+template <class U_>
+__device__ __forceinline__ Cursor<U_> locate(const PagedArgs &p, int HH, int place, int left) {
     const int lane = threadIdx.x & 31;
-    Cursor<kUnit> at = {0, 0, 0, 1, 0};
-    int before = 0;  // (in units of one head)
+    Cursor<U_> at = {0, 0, 0, 1, 0, 0};
+    int before = 0;  // (of one head)
     for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
         const int i = b0 + lane;
         const int len = i < p.n_seq ? seq_len(p, i, false) : 0;
-        const int U = units_of<kUnit>(len);
-        int incl = U;
+        const int n = U_::places(len);
+        int incl = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += o;
         }
-        const unsigned m = __ballot_sync(0xffffffffu, (before + incl) * HH > unit);
+        const unsigned m = __ballot_sync(0xffffffffu, (before + incl) * HH > place);
         if (m) {
             const int l = __ffs(m) - 1;
             at.b = b0 + l;
-            at.U = __shfl_sync(0xffffffffu, U, l);
             at.len = __shfl_sync(0xffffffffu, len, l);
-            const int rest = unit - (before + __shfl_sync(0xffffffffu, incl - U, l)) * HH;
-            at.hh = rest / at.U;
-            at.u = rest - at.hh * at.U;
+            at.U = U_::of(at.len);
+            const int rest = place - (before + __shfl_sync(0xffffffffu, incl - n, l)) * HH;
+            const int each = at.U + U_::kExtra;
+            at.hh = rest / each;
+            const int j = rest - at.hh * each;  // place of the item
+            at.u = max(j - U_::kExtra, 0);
+            at.left = max(left - max(U_::kExtra - j, 0), 0);
             break;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -153,14 +151,13 @@ __device__ __forceinline__ Cursor<kUnit> locate(const PagedArgs &p, int HH, int 
     return at;
 }
 
-// Sets a.ways for units of `unit` rows and at most `most` CTAs; false (and a.taken
-// NULL) where every CTA keeps to its share.
-bool paged_ways(PagedArgs &a, int unit, int most);
-cudaError_t launch_paged_begin(const PagedArgs &a, const LaunchCtx &ctx);
+// The CTAs of a launch: as many as there can be units, at most `most`.
+int paged_ways(const PagedArgs &a, int rows, int most);
 
-// The tcgen05 kernel (paged_attn_tc.cu): 8-bit rows of 128 elements.  *block_heads:
-// the heads of a partial result.
-constexpr int kPagedTcUnit = 128;
+// The tcgen05 kernel (paged_attn_tc.cu): 8-bit rows of 128 elements.  An item costs
+// about what a unit does: the queries' way into shared memory, the first maximum,
+// the joined output.  *block_heads: the heads of a partial result.
+using TcUnits = Units<256, 1>;
 cudaError_t launch_paged_tc(PagedArgs &a, const KvCacheSpec &cache, const LaunchCtx &ctx,
                             int *block_heads);
 

@@ -1,11 +1,11 @@
 // paged_attn_tc.cu -- attention of one token over an 8-bit cache of 128-element
 // heads on tcgen05 (the split and the join: paged_attn.cu).
 //
-// Reading the cache at HBM's rate leaves an SM about 1400 cycles for a unit of 128
-// rows of one kv head (32 KB), too few to convert 8-bit elements for a 16-bit MMA
-// in registers: that took about 470 warp instructions for every 16 rows, and was
-// what bounded the kernel.  Here the tensor core reads the elements as TMA left
-// them in shared memory (kind::f8f6f4), and the threads see scores and weights alone:
+// Reading the cache at HBM's rate leaves an SM about 1400 cycles for 128 rows of one kv
+// head (32 KB), too few to convert 8-bit elements for a 16-bit MMA in registers: that
+// took about 470 warp instructions for every 16 rows, and was what bounded the
+// kernel.  Here the tensor core reads the elements as TMA left them in shared memory
+// (kind::f8f6f4), and the threads see scores and weights alone:
 //   S[row, col]  = K[row, :] . Qt[col, :]     128 rows, 16 or 32 columns
 //   Ot[d, col]  += sum_row V[row, d] Pt[col, row]
 // Both other operands become several e4m3 terms, each in columns of its own:
@@ -18,11 +18,19 @@
 // of its weight, w = 2^(s + e - m), with m the running maximum of s + e, while the sum
 // takes 2^(s - m) in fp32.  m moves only by more than 1, so weights stay below 2.
 //
-// Roles: warps 0-3 softmax and output (thread = cache row of a unit, then = element of
-// O); warp 4 looks up pages, starts the loads (a queue of kStages units, which keeps
-// 160 KB in flight) and lays out the next item's queries; warp 5 issues the MMAs, the
-// scores of unit i + 1 before the product of unit i, so that softmax never waits for
-// them.  What a unit is goes along with it in the queue, so only warp 4 knows the
+// A unit is 256 rows, two MMAs' worth: each role's waits and bookkeeping take it about
+// 1000 cycles a unit, whatever its size.
+//
+// Roles: warps 0-3 and 4-7 softmax and output, two groups that take turns (thread = two
+// cache rows of a unit, then = element of O), since a unit's chain of dependent
+// instructions is longer than its share of HBM.  Each group has its own m, sum and
+// O; where an item ends they are joined.  Warp 8 looks up pages, starts the loads of
+// keys and lays out the next item's queries; warp 11 starts the loads of scales and values
+// (a TMA instruction takes its lanes one after another, about 100 cycles each); warp 9
+// issues the MMAs of the scores, up to four units ahead of the products, which warp 10
+// issues.  Keys' places are free once their scores are done, values are waited for
+// where the product needs them, not before, so that most of the queue's bytes are in
+// flight.  What a unit is goes along with it in the queue, so only warp 8 knows the
 // split.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -38,52 +46,73 @@
 namespace wanvae {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kStages = 6;
-constexpr int kUnit = kPagedTcUnit;
-constexpr uint32_t kTileBytes = kUnit * 128;  // keys, or values, of a unit
+constexpr int kThreads = 384;
+constexpr int kUnit = TcUnits::kRows, kHalves = kUnit / 128;
+constexpr uint32_t kHalfBytes = 128 * 128;              // 128 rows of keys, or values
+constexpr uint32_t kTileBytes = kHalves * kHalfBytes;   // of a unit
+constexpr int kBoxes = kUnit / 16;                      // boxes of a unit, at most
 
 // What the queue tells of a unit.
 struct Unit {
     int b, head0, heads;  // sequence, first query head, heads of the item
     int rows;             // rows that count (the unit's first)
-    uint32_t missing;     // groups of 16 rows whose page is not there
+    uint32_t missing;     // boxes whose page is not there
     int slot;             // of the partial result
     int flags;
-    int pad;
+    int item;             // number of the item in this CTA
 };
-enum : int { kFirst = 1, kLast = 2, kWhole = 4, kEnd = 8 };
+// The item's first two units (each group's first), its last two (each group's last;
+// kLast alone where it has one), whether a range holds it whole, the end of all.
+enum : int { kFirst = 1, kSecond = 2, kLast = 4, kLastBut1 = 8, kWhole = 16, kEnd = 32 };
 
 // HP: query heads of an item, at most (4, 8 or 16).
 template <int HP>
 struct Cfg {
     static constexpr int N1 = 2 * HP < 16 ? 16 : 2 * HP;         // columns of S
     static constexpr int N2 = (3 * HP + 15) / 16 * 16;           // columns of O
-    static constexpr uint32_t kP = kStages * 2 * kTileBytes;     // [2][N2][128 rows]
+    // Places for keys, which the scores free, and for values and what is told of a
+    // unit, which the products free.
+    static constexpr int kKeys = 2, kStages = HP > 8 ? 3 : 4;
+    static constexpr uint32_t kV = kKeys * kTileBytes;
+    static constexpr uint32_t kP = kV + kStages * kTileBytes;    // [groups][halves][N2][128 rows]
     static constexpr uint32_t kPBytes = N2 * 128;
-    static constexpr uint32_t kQ = kP + 2 * kPBytes;             // [2][N1][128 elements]
+    static constexpr uint32_t kQ = kP + 2 * kHalves * kPBytes;   // [2][N1][128 elements]
     static constexpr uint32_t kQBytes = N1 * 128;
-    static constexpr uint32_t kExp = kQ + 2 * kQBytes;           // [stages][2][128]
-    static constexpr uint32_t kMeta = kExp + kStages * 256;
-    static constexpr uint32_t kQs = kMeta + kStages * sizeof(Unit);  // [2][16] floats
-    static constexpr uint32_t kRed = kQs + 128;                  // [2][4][16] floats
-    static constexpr uint32_t kBars = kRed + 512;
-    static constexpr uint32_t kSlots = kBars + 8 * (2 * kStages + 13);
+    static constexpr uint32_t kExp = kQ + 2 * kQBytes;           // [stages][2][rows]
+    static constexpr uint32_t kMeta = kExp + kStages * 2 * kUnit;
+    static constexpr uint32_t kPages = kMeta + kStages * sizeof(Unit);  // [stages][page, row]
+    static constexpr uint32_t kQs = kPages + kStages * kBoxes * 8;  // [2][16] floats
+    static constexpr uint32_t kRed = kQs + 128;                  // [groups][2][4][16] floats
+    static constexpr uint32_t kJoin = kRed + 1024;               // [HP][128 + maximum, sum]
+    static constexpr uint32_t kBars = kJoin + HP * 130 * 4;
+    static constexpr uint32_t kSlots = kBars + 8 * (2 * kKeys + 4 * kStages + 20);
     static constexpr uint32_t kSmem = 1024 + kSlots + 16;
-    static constexpr uint32_t kTmemO = 64;  // S at columns 0 and 32, O behind
+    // TMEM: S of half h of units i % 4 at columns 64 (i % 4) + 32 h, then each group's O
+    static __device__ __forceinline__ uint32_t s_col(int i) { return 64u * i; }
+    static __device__ __forceinline__ uint32_t o_col(int w) { return 256u + 48u * w; }
 };
 
+template <int HP>
 struct Bars {
+    static constexpr int kKeys = Cfg<HP>::kKeys, kStages = Cfg<HP>::kStages;
     uint32_t base;
-    __device__ uint32_t full(int s) const { return base + 8 * s; }
-    __device__ uint32_t empty(int s) const { return base + 8 * (kStages + s); }
-    __device__ uint32_t q_ready(int i) const { return base + 8 * (2 * kStages + i); }
-    __device__ uint32_t q_free(int i) const { return base + 8 * (2 * kStages + 2 + i); }
-    __device__ uint32_t s_full(int i) const { return base + 8 * (2 * kStages + 4 + i); }
-    __device__ uint32_t s_free(int i) const { return base + 8 * (2 * kStages + 6 + i); }
-    __device__ uint32_t p_full(int i) const { return base + 8 * (2 * kStages + 8 + i); }
-    __device__ uint32_t pv_done(int i) const { return base + 8 * (2 * kStages + 10 + i); }
-    __device__ uint32_t drain() const { return base + 8 * (2 * kStages + 12); }
+    __device__ uint32_t at(int i) const { return base + 8 * i; }
+    __device__ uint32_t k_full(int s) const { return at(s); }
+    __device__ uint32_t k_empty(int s) const { return at(kKeys + s); }
+    __device__ uint32_t v_full(int s) const { return at(2 * kKeys + s); }
+    __device__ uint32_t v_empty(int s) const { return at(2 * kKeys + kStages + s); }
+    __device__ uint32_t posted(int s) const { return at(2 * kKeys + 2 * kStages + s); }
+    __device__ uint32_t told(int s) const { return at(2 * kKeys + 3 * kStages + s); }
+    __device__ uint32_t more(int i) const { return at(2 * kKeys + 4 * kStages + i); }
+    __device__ uint32_t q_ready(int i) const { return more(i); }
+    __device__ uint32_t q_free(int i) const { return more(2 + i); }
+    __device__ uint32_t s_full(int i) const { return more(4 + i); }
+    __device__ uint32_t s_free(int i) const { return more(8 + i); }
+    __device__ uint32_t p_full(int w) const { return more(12 + w); }
+    __device__ uint32_t pv_done(int w) const { return more(14 + w); }
+    __device__ uint32_t join_full() const { return more(16); }
+    __device__ uint32_t join_free() const { return more(17); }
+    __device__ uint32_t drain(int i) const { return more(18 + i); }
 };
 
 // A place in a ring of n, and the parity of its turn.
@@ -91,9 +120,10 @@ template <int n>
 struct Turn {
     int i = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++i == n) {
-            i = 0;
+    __device__ __forceinline__ void next(int by = 1) {
+        i += by;
+        if (i >= n) {
+            i -= n;
             phase ^= 1u;
         }
     }
@@ -146,8 +176,8 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t *
         : "memory");
 }
 
-__device__ __forceinline__ void bar_softmax() {
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+__device__ __forceinline__ void bar_group(int w) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -161,379 +191,538 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// Warp 4: units into the queue, range after range.
+// 8 bytes of global memory to shared memory, and this thread's arrival on `bar` once
+// its copies so far are done.
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Aborted: lets every copy in flight land before shared memory goes away.
 template <int HP>
-__device__ void feed(const CUtensorMap *mK, const CUtensorMap *mV, const PagedArgs &p,
-                     int log2_box, uint8_t *smem, const Bars &bars, const WaitCtl &wc) {
+__device__ __forceinline__ void drain_loads(int fills, const Bars<HP> &bars, bool values,
+                                            const WaitCtl &wc) {
+    volatile int no_abort = 0;
+    const WaitCtl dc{kPagedDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
+    const int n = values ? bars.kStages : bars.kKeys;
+    for (int i = fills > n ? fills - n : 0; i < fills; ++i)
+        mbar_wait<false>(values ? bars.v_full(i % n) : bars.k_full(i % n), (uint32_t)(i / n) & 1u,
+                         dc);
+}
+
+// Warp 8: the share's units into the queue (their keys; the rest is warp 11's).
+template <int HP>
+__device__ void feed(const CUtensorMap *mK, const PagedArgs &p, int log2_box,
+                     uint8_t *smem, const Bars<HP> &bars, const WaitCtl &wc) {
     using C = Cfg<HP>;
     const int lane = threadIdx.x & 31;
     const uint32_t sbase = smem_u32(smem);
     const int HH = p.H * p.HB;
-    const int total = units_before<kUnit>(p, p.n_seq, blockIdx.x == 0) * HH;
-    const Split split(total, p.ways, p.taken != nullptr);
+    const int total = TcUnits::before(p, p.n_seq, blockIdx.x == 0) * HH;
+    const Split split(total, p.ways);
     Unit *queue = reinterpret_cast<Unit *>(smem + C::kMeta);
-    Turn<kStages> put;
+    Turn<C::kStages> put;
+    Turn<C::kKeys> key;
     Turn<2> item;
-    int fills = 0;
+    int fills = 0, items = 0, nth = 0;  // nth: of the item's units
     bool ok = true;
-    int range = (int)blockIdx.x < split.ways && total > 0 ? split.own(blockIdx.x) : split.ranges;
-    while (ok && range < split.ranges) {
-        int left = split.begin(range + 1) - split.begin(range);
-        Cursor<kUnit> at = locate<kUnit>(p, HH, split.begin(range));
-        bool first_item = true, starts = true, whole = false;
-        // the page of box `lane` of the unit to come
-        const int boxes = kUnit >> log2_box;
-        auto find_page = [&]() -> int {
-            const int tok = at.u * kUnit + (lane << log2_box);
-            if (lane >= boxes || tok >= at.len) return -2;
-            return __ldg(p.table + (int64_t)at.b * p.max_pages + (tok >> p.log2_page));
-        };
-        int page = find_page();
-        while (left > 0) {
-            const int kvh = at.hh / p.HB, head0 = kvh * p.G + (at.hh - kvh * p.HB) * HP;
-            const int heads = min(HP, (kvh + 1) * p.G - head0);
-            if (starts) whole = at.u == 0 && at.U <= left;  // the range holds the item
-            ok = mbar_wait_warp<false>(bars.empty(put.i), put.phase ^ 1u, wc);
-            if (!ok) break;
-            const bool wanted = page != -2, there = (unsigned)page < (unsigned)p.n_pages;
-            if (wanted && !there) atomicOr(p.err, kDevErrAlign);
-            const uint32_t gone = __ballot_sync(0xffffffffu, wanted && !there);
-            const int loads = __popc(__ballot_sync(0xffffffffu, there));
-            if (lane == 0) {
-                Unit u;
-                u.b = at.b;
-                u.head0 = head0;
-                u.heads = heads;
-                u.rows = min(at.len - at.u * kUnit, kUnit);
-                u.missing = gone;
-                u.slot = (2 * range + (first_item ? 0 : 1)) * HP;
-                u.flags = (starts ? kFirst : 0) | (at.u + 1 == at.U || left == 1 ? kLast : 0) |
-                          (whole ? kWhole : 0);
-                u.pad = 0;
-                queue[put.i] = u;
-                mbar_arrive_expect_tx(bars.full(put.i), (uint32_t)loads * (258u << log2_box));
-            }
-            __syncwarp();
-            if (there) {
-                const int row = (kvh << p.log2_page) +
-                                ((at.u * kUnit + (lane << log2_box)) & ((1 << p.log2_page) - 1));
-                const uint32_t dst = sbase + put.i * 2 * kTileBytes + ((uint32_t)lane << (log2_box + 7));
-                const uint32_t ex = sbase + C::kExp + put.i * 256 + (lane << log2_box);
-                const uint32_t bar = bars.full(put.i);
-                tma_load_3d(dst, mK, bar, 0, row, page);
-                tma_load_3d(dst + kTileBytes, mV, bar, 0, row, page);
-                const int64_t at_row = (((int64_t)page * p.H) << p.log2_page) + row;
-                bulk_load(ex, p.k_exp + at_row, 1u << log2_box, bar);
-                bulk_load(ex + 128, p.v_exp + at_row, 1u << log2_box, bar);
-            }
-            ++fills;
-            put.next();
-            if (starts) {
-                // the item's queries, as e4m3 terms: rows h and HP + h of its buffer
-                uint2 raw[HP];
-                const __nv_bfloat16 *src =
-                    p.q + (int64_t)at.b * p.q_stride + (int64_t)head0 * 128 + lane * 4;
-#pragma unroll
-                for (int h = 0; h < HP; ++h)
-                    raw[h] = h < heads ? __ldg(reinterpret_cast<const uint2 *>(src + h * 128))
-                                       : make_uint2(0u, 0u);
-                ok = mbar_wait_warp<false>(bars.q_free(item.i), item.phase ^ 1u, wc);
-                if (!ok) break;
-                uint8_t *dst = smem + C::kQ + item.i * C::kQBytes;
-                float *qs = reinterpret_cast<float *>(smem + C::kQs) + item.i * 16;
-#pragma unroll
-                for (int h = 0; h < HP; ++h) {
-                    uint32_t amax = max(max(raw[h].x & 0x7fffu, (raw[h].x >> 16) & 0x7fffu),
-                                        max(raw[h].y & 0x7fffu, (raw[h].y >> 16) & 0x7fffu));
-                    amax = __reduce_max_sync(0xffffffffu, amax);
-                    // 2^(7 - exponent of the largest); both powers stay in fp32's range
-                    const int ex = min(max((int)(amax >> 7), 8), 254) - 127 - 7;
-                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                    const float x[4] = {nact_lo(raw[h].x) * down, nact_hi(raw[h].x) * down,
-                                        nact_lo(raw[h].y) * down, nact_hi(raw[h].y) * down};
-                    const uint32_t a = f32x2_to_e4m3x2(x[0], x[1]), b = f32x2_to_e4m3x2(x[2], x[3]);
-                    const float2 ya = e4m3x2_to_f32(a), yb = e4m3x2_to_f32(b);
-                    const uint32_t ra = f32x2_to_e4m3x2(32.f * (x[0] - ya.x), 32.f * (x[1] - ya.y));
-                    const uint32_t rb = f32x2_to_e4m3x2(32.f * (x[2] - yb.x), 32.f * (x[3] - yb.y));
-                    auto place = [&](int n) {
-                        return dst + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4;
-                    };
-                    *reinterpret_cast<uint32_t *>(place(h)) = a | (b << 16);
-                    *reinterpret_cast<uint32_t *>(place(HP + h)) = ra | (rb << 16);
-                    if (lane == 0)  // (a query that is not finite has no scores)
-                        qs[h] = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u)
-                                                : p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.q_ready(item.i));
-                item.next();
-                starts = false;
-            }
-            if (--left > 0) {
-                if (at.next(p, HH)) {
-                    starts = true;
-                    first_item = false;
-                }
-                page = find_page();
-            }
+    const int begin = split.begin(blockIdx.x);
+    Cursor<TcUnits> at = {0, 0, 0, 1, 0, 0};
+    if ((int)blockIdx.x < split.ways && total > 0)
+        at = locate<TcUnits>(p, HH, begin, split.begin(blockIdx.x + 1) - begin);
+    bool first_item = true, starts = true, whole = false;
+    // The pages of the item's boxes `base` .. + 31 and of the 32 behind them, one a
+    // lane: looked up this far ahead, the loop does not wait for them unit by unit.
+    const int boxes = kUnit >> log2_box;
+    auto look_up = [&](int box) -> int {
+        const int64_t tok = (int64_t)(box + lane) << log2_box;
+        if (tok >= at.len) return -2;
+        return __ldg(p.table + (int64_t)at.b * p.max_pages + (tok >> p.log2_page));
+    };
+    int base = (at.u * boxes) & ~31;
+    int pages = look_up(base), more_pages = look_up(base + 32);
+    Unit u = {};  // (what an item's units have alike is set where it starts)
+    int row0 = 0;
+    while (at.left > 0) {
+        if (starts) {
+            const int kvh = at.hh / p.HB;
+            row0 = kvh << p.log2_page;
+            u.b = at.b;
+            u.head0 = kvh * p.G + (at.hh - kvh * p.HB) * HP;
+            u.heads = min(HP, (kvh + 1) * p.G - u.head0);
+            u.slot = (2 * blockIdx.x + (first_item ? 0 : 1)) * HP;
+            u.item = items;
+            whole = at.u == 0 && at.U <= at.left;  // the share holds the item
         }
+        // box `lane` of this unit
+        const int box0 = at.u * boxes - base + lane;
+        int page = __shfl_sync(0xffffffffu, pages, box0 & 31);
+        if (lane >= boxes) page = -2;
+        const int row = row0 + ((at.u * kUnit + (lane << log2_box)) & ((1 << p.log2_page) - 1));
+        const bool wanted = page != -2, there = (unsigned)page < (unsigned)p.n_pages;
+        if (wanted && !there) atomicOr(p.err, kDevErrAlign);
+        const uint32_t gone = __ballot_sync(0xffffffffu, wanted && !there);
+        const int loads = __popc(__ballot_sync(0xffffffffu, there));
+        const int more = at.units() - 1;  // units of the item behind it
+        u.rows = min(at.len - at.u * kUnit, kUnit);
+        u.missing = gone;
+        u.flags = (nth == 0 ? kFirst : 0) | (nth == 1 ? kSecond : 0) |
+                  (more == 0 ? kLast : 0) | (more == 1 ? kLastBut1 : 0) | (whole ? kWhole : 0);
+        ok = mbar_wait_warp<false>(bars.k_empty(key.i), key.phase ^ 1u, wc) &&
+             mbar_wait_warp<false>(bars.v_empty(put.i), put.phase ^ 1u, wc);
         if (!ok) break;
-        range = split.ranges;
-        if (split.small) {
-            if (lane == 0) range = split.taken(atomicAdd(p.taken, 1));
-            range = __shfl_sync(0xffffffffu, range, 0);
-        }
-    }
-    if (ok) ok = mbar_wait_warp<false>(bars.empty(put.i), put.phase ^ 1u, wc);
-    if (ok) {
+        if (lane < boxes)
+            reinterpret_cast<int2 *>(smem + C::kPages)[put.i * kBoxes + lane] =
+                make_int2(there ? page : -1, row);
         if (lane == 0) {
-            queue[put.i].flags = kEnd;
-            mbar_arrive(bars.full(put.i));
+            queue[put.i] = u;
+            mbar_arrive_expect_tx(bars.k_full(key.i), (uint32_t)loads << (log2_box + 7));
         }
-    } else if (lane == 0) {
-        // Aborted: let every copy in flight land before shared memory goes away.
-        volatile int no_abort = 0;
-        const WaitCtl dc{kPagedDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
-        for (int i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
-            mbar_wait<false>(bars.full(i % kStages), (uint32_t)(i / kStages) & 1u, dc);
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bars.posted(put.i));
+            mbar_arrive(bars.told(put.i));
+        }
+        if (there)
+            tma_load_3d(sbase + key.i * kTileBytes + ((uint32_t)lane << (log2_box + 7)), mK,
+                        bars.k_full(key.i), 0, row, page);
+        ++fills;
+        ++nth;
+        put.next();
+        key.next();
+        if (starts) {
+            // the item's queries, as e4m3 terms: rows h and HP + h of its buffer
+            uint2 raw[HP];
+            const __nv_bfloat16 *src =
+                p.q + (int64_t)u.b * p.q_stride + (int64_t)u.head0 * 128 + lane * 4;
+#pragma unroll
+            for (int h = 0; h < HP; ++h)
+                raw[h] = h < u.heads ? __ldg(reinterpret_cast<const uint2 *>(src + h * 128))
+                                   : make_uint2(0u, 0u);
+            ok = mbar_wait_warp<false>(bars.q_free(item.i), item.phase ^ 1u, wc);
+            if (!ok) break;
+            uint8_t *dst = smem + C::kQ + item.i * C::kQBytes;
+            float *qs = reinterpret_cast<float *>(smem + C::kQs) + item.i * 16;
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+                uint32_t amax = max(max(raw[h].x & 0x7fffu, (raw[h].x >> 16) & 0x7fffu),
+                                    max(raw[h].y & 0x7fffu, (raw[h].y >> 16) & 0x7fffu));
+                amax = __reduce_max_sync(0xffffffffu, amax);
+                // 2^(7 - exponent of the largest); both powers stay in fp32's range
+                const int ex = min(max((int)(amax >> 7), 8), 254) - 127 - 7;
+                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                const float x[4] = {nact_lo(raw[h].x) * down, nact_hi(raw[h].x) * down,
+                                    nact_lo(raw[h].y) * down, nact_hi(raw[h].y) * down};
+                const uint32_t a = f32x2_to_e4m3x2(x[0], x[1]), b = f32x2_to_e4m3x2(x[2], x[3]);
+                const float2 ya = e4m3x2_to_f32(a), yb = e4m3x2_to_f32(b);
+                const uint32_t ra = f32x2_to_e4m3x2(32.f * (x[0] - ya.x), 32.f * (x[1] - ya.y));
+                const uint32_t rb = f32x2_to_e4m3x2(32.f * (x[2] - yb.x), 32.f * (x[3] - yb.y));
+                auto place = [&](int n) {
+                    return dst + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4;
+                };
+                *reinterpret_cast<uint32_t *>(place(h)) = a | (b << 16);
+                *reinterpret_cast<uint32_t *>(place(HP + h)) = ra | (rb << 16);
+                if (lane == 0)  // (a query that is not finite has no scores)
+                    qs[h] = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                            : p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.q_ready(item.i));
+            item.next();
+            starts = false;
+        }
+        if (at.next(p, HH, 1)) {
+            starts = true;
+            first_item = false;
+            nth = 0;
+            ++items;
+            base = 0;
+            if (at.left > 0) {
+                pages = look_up(0);
+                more_pages = look_up(32);
+            }
+        } else if (at.u * boxes >= base + 32) {
+            base += 32;
+            pages = more_pages;
+            more_pages = look_up(base + 32);
+        }
     }
+    for (int w = 0; ok && w < 2; ++w) {  // both groups are told
+        ok = mbar_wait_warp<false>(bars.k_empty(key.i), key.phase ^ 1u, wc) &&
+             mbar_wait_warp<false>(bars.v_empty(put.i), put.phase ^ 1u, wc);
+        if (ok) {
+            if (lane == 0) {
+                queue[put.i].flags = kEnd;
+                mbar_arrive(bars.posted(put.i));
+                mbar_arrive(bars.k_full(key.i));
+                mbar_arrive(bars.told(put.i));
+            }
+        }
+        put.next();
+        key.next();
+    }
+    if (!ok && lane == 0) drain_loads(fills, bars, false, wc);
 }
 
-// Warp 5, one thread: the MMAs.
+// Warp 11: the scales and values of the units that warp 8 posts.
 template <int HP>
-__device__ void issue(uint8_t *smem, uint32_t tmem, const Bars &bars, const WaitCtl &wc) {
+__device__ void feed_values(const CUtensorMap *mV, const PagedArgs &p, int log2_box, uint8_t *smem,
+                            const Bars<HP> &bars, const WaitCtl &wc) {
+    using C = Cfg<HP>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(smem);
+    const Unit *queue = reinterpret_cast<const Unit *>(smem + C::kMeta);
+    Turn<C::kStages> put;
+    int fills = 0, ends = 0;
+    bool ok = true;
+    while (ends < 2) {
+        ok = mbar_wait_warp<false>(bars.posted(put.i), put.phase, wc);
+        if (!ok) break;
+        const uint32_t bar = bars.v_full(put.i);
+        if (queue[put.i].flags & kEnd) {
+            if (lane == 0) mbar_arrive(bar);
+            mbar_arrive(bars.told(put.i));  // (as many arrivals as a unit has)
+            ++ends;
+        } else {
+            const int2 *said = reinterpret_cast<const int2 *>(smem + C::kPages) + put.i * kBoxes;
+            const int2 box = lane < (kUnit >> log2_box) ? said[lane] : make_int2(-1, 0);
+            const int2 box8 = said[(lane * 8) >> log2_box];  // of rows 8 lane .. + 7
+            if (box8.x >= 0) {
+                const int64_t at_row = (((int64_t)box8.x * p.H) << p.log2_page) + box8.y +
+                                       ((lane * 8) & ((1 << log2_box) - 1));
+                const uint32_t ex = sbase + C::kExp + put.i * 2 * kUnit + lane * 8;
+                copy8(ex, p.k_exp + at_row);
+                copy8(ex + kUnit, p.v_exp + at_row);
+            }
+            arrive_after_copies(bars.told(put.i));
+            const int loads = __popc(__ballot_sync(0xffffffffu, box.x >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)loads << (log2_box + 7));
+            __syncwarp();
+            if (box.x >= 0)
+                tma_load_3d(sbase + C::kV + put.i * kTileBytes + ((uint32_t)lane << (log2_box + 7)),
+                            mV, bar, 0, box.y, box.x);
+            ++fills;
+        }
+        put.next();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) drain_loads(fills, bars, true, wc);
+}
+
+// Every MMA that this thread issued completes before TMEM is released.
+__device__ __forceinline__ void drain_mmas(uint32_t bar, const WaitCtl &wc) {
+    volatile int no_abort = 0;
+    const WaitCtl dc{kPagedDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
+    mma_commit(bar);
+    mbar_wait<false>(bar, 0u, dc);
+}
+
+// Warp 9, one thread: the scores.
+template <int HP>
+__device__ void issue_scores(uint8_t *smem, uint32_t tmem, const Bars<HP> &bars, const WaitCtl &wc) {
     using C = Cfg<HP>;
     const uint32_t sbase = smem_u32(smem);
     const Unit *queue = reinterpret_cast<const Unit *>(smem + C::kMeta);
-    const uint32_t id_s = idesc_e4m3(C::N1, false), id_o = idesc_e4m3(C::N2, true);
+    const uint32_t id = idesc_e4m3(C::N1, false);
     const uint64_t k0 = sdesc_kmajor(sbase, 128u, kLayoutSw128);
-    const uint64_t v0 = sdesc_rows_sw128(sbase + kTileBytes, kTileBytes);
     const uint64_t q0 = sdesc_kmajor(sbase + C::kQ, 128u, kLayoutSw128);
-    const uint64_t p0 = sdesc_kmajor(sbase + C::kP, 128u, kLayoutSw128);
-    Turn<kStages> get;
-    Turn<2> item, buf, last_buf;
-    int last_stage = -1, last_first = 0;
-    bool ok = true;
-    auto product = [&]() -> bool {  // of the unit before
-        if (!mbar_wait<false>(bars.p_full(last_buf.i), last_buf.phase, wc)) return false;
-        tc_fence_after();
-        const uint64_t a = v0 + (uint32_t)last_stage * (2 * kTileBytes >> 4);
-        const uint64_t b = p0 + (uint32_t)last_buf.i * (C::kPBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < kUnit / 32; ++k)
-            mma_e4m3_ss(tmem + C::kTmemO, a + k * (32 * 128 >> 4), b + k * 2, id_o,
-                        !last_first || k > 0);
-        mma_commit(bars.empty(last_stage));
-        mma_commit(bars.pv_done(last_buf.i));
-        last_buf.next();
-        return true;
-    };
-    while (true) {
-        ok = mbar_wait<false>(bars.full(get.i), get.phase, wc);
-        if (!ok) break;
-        const int flags = queue[get.i].flags;
-        if (flags & kEnd) {
-            if (last_stage >= 0) ok = product();
+    Turn<C::kStages> get;
+    Turn<C::kKeys> key;
+    Turn<4> buf;
+    while (mbar_wait<false>(bars.k_full(key.i), key.phase, wc)) {
+        const int flags = queue[get.i].flags, item = queue[get.i].item;
+        if (flags & kEnd) break;
+        if ((flags & kFirst) &&
+            !mbar_wait<false>(bars.q_ready(item & 1), (uint32_t)(item >> 1) & 1u, wc))
             break;
-        }
-        if (flags & kFirst) ok = mbar_wait<false>(bars.q_ready(item.i), item.phase, wc);
-        ok = ok && mbar_wait<false>(bars.s_free(buf.i), buf.phase ^ 1u, wc);
-        if (!ok) break;
+        if (!mbar_wait<false>(bars.s_free(buf.i), buf.phase ^ 1u, wc)) break;
         tc_fence_after();
-        const uint64_t a = k0 + (uint32_t)get.i * (2 * kTileBytes >> 4);
-        const uint64_t b = q0 + (uint32_t)item.i * (C::kQBytes >> 4);
+        const uint64_t a = k0 + (uint32_t)key.i * (kTileBytes >> 4);
+        const uint64_t b = q0 + (uint32_t)(item & 1) * (C::kQBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_e4m3_ss(tmem + 32u * buf.i, a + k * 2, b + k * 2, id_s, k > 0);
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_e4m3_ss(tmem + C::s_col(buf.i) + 32u * h, a + h * (kHalfBytes >> 4) + k * 2,
+                            b + k * 2, id, k > 0);
         mma_commit(bars.s_full(buf.i));
-        if (flags & kLast) {
-            mma_commit(bars.q_free(item.i));
-            item.next();
-        }
-        if (last_stage >= 0) ok = product();
-        if (!ok) break;
-        last_stage = get.i;
-        last_first = flags & kFirst;
+        mma_commit(bars.k_empty(key.i));
+        if (flags & kLast) mma_commit(bars.q_free(item & 1));
         buf.next();
         get.next();
+        key.next();
     }
-    // Every MMA issued above completes before TMEM is released.
-    volatile int no_abort = 0;
-    const WaitCtl dc{kPagedDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
-    mma_commit(bars.drain());
-    mbar_wait<false>(bars.drain(), 0u, dc);
+    drain_mmas(bars.drain(0), wc);
 }
 
-// Warps 0-3.  Thread r: row r of a unit, and element r of the outputs.  A warp
-// whose wait runs out does no more work, but keeps to the barriers until all four
-// learn of it and leave together.
+// Warp 10, one thread: the products.
 template <int HP>
-__device__ void softmax(const PagedArgs &p, uint8_t *smem, uint32_t tmem, const Bars &bars,
-                        const WaitCtl &wc) {
+__device__ void issue_products(uint8_t *smem, uint32_t tmem, const Bars<HP> &bars, const WaitCtl &wc) {
     using C = Cfg<HP>;
-    const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
-    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t sbase = smem_u32(smem);
     const Unit *queue = reinterpret_cast<const Unit *>(smem + C::kMeta);
-    float *red = reinterpret_cast<float *>(smem + C::kRed);
+    const uint32_t id = idesc_e4m3(C::N2, true);
+    const uint64_t v0 = sdesc_rows_sw128(sbase + C::kV, kHalfBytes);
+    const uint64_t p0 = sdesc_kmajor(sbase + C::kP, 128u, kLayoutSw128);
+    Turn<C::kStages> get;
+    Turn<2> w;
+    while (mbar_wait<false>(bars.v_full(get.i), get.phase, wc)) {
+        const int flags = queue[get.i].flags;
+        if ((flags & kEnd) || !mbar_wait<false>(bars.p_full(w.i), w.phase, wc)) break;
+        tc_fence_after();
+        const uint32_t more = (flags & (kFirst | kSecond)) ? 0u : 1u;
+        const uint64_t a = v0 + (uint32_t)get.i * (kTileBytes >> 4);
+        const uint64_t b = p0 + (uint32_t)w.i * (kHalves * C::kPBytes >> 4);
+        const uint32_t d = tmem + C::o_col(w.i);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_e4m3_ss(d, a + h * (kHalfBytes >> 4) + k * (32 * 128 >> 4),
+                            b + h * (C::kPBytes >> 4) + k * 2, id, h + k > 0 ? 1u : more);
+        mma_commit(bars.pv_done(w.i));
+        mma_commit(bars.v_empty(get.i));
+        w.next();
+        get.next();
+    }
+    drain_mmas(bars.drain(1), wc);
+}
+
+// Group w (warps 4 w .. 4 w + 3): every second unit.  Thread r: rows r and r + 128 of a
+// unit, and element r of the outputs.  A warp whose wait runs out does no more work, but keeps
+// to the group's barriers until all four learn of it and leave together.
+template <int HP>
+__device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
+                        const Bars<HP> &bars, const WaitCtl &wc) {
+    using C = Cfg<HP>;
+    const int r = threadIdx.x & 127, warp = r >> 5, lane = r & 31;
+    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t to = trow + C::o_col(w);
+    const Unit *queue = reinterpret_cast<const Unit *>(smem + C::kMeta);
+    float *red = reinterpret_cast<float *>(smem + C::kRed) + w * 128;
+    float *join = reinterpret_cast<float *>(smem + C::kJoin);
     // the place of this row in P's rows n (128-byte swizzle)
     uint32_t place[8];
 #pragma unroll
     for (int n = 0; n < 8; ++n) place[n] = n * 128 + (((r >> 4) ^ n) << 4) + (r & 15);
-    Turn<kStages> get;
-    Turn<2> item, buf;
-    float qs[HP], m[HP], l[HP], s[HP];
+    Turn<C::kStages> get;
+    get.i = w;
+    Turn<4> buf;
+    buf.i = w;
+    Turn<1> turn, joins;  // parities alone
+    const int log2_box = min(p.log2_page, 7);
+    float qs[HP], m[HP], l[HP], s[kHalves][HP];
 #pragma unroll
-    for (int h = 0; h < HP; ++h) qs[h] = m[h] = l[h] = s[h] = 0.f;
+    for (int h = 0; h < HP; ++h) qs[h] = m[h] = l[h] = s[0][h] = s[kHalves - 1][h] = 0.f;
     bool ok = true;
     while (true) {
-        ok = ok && mbar_wait_warp<false>(bars.full(get.i), get.phase, wc);
+        ok = ok && mbar_wait_warp<false>(bars.told(get.i), get.phase, wc);
         Unit u = {0, 0, 0, 0, 0u, 0, 0, 0};
         if (ok) u = queue[get.i];
-        const bool end = (u.flags & kEnd) != 0;
-        float ve = 0.f;
-        bool there = false, moves = false;
+        const bool end = (u.flags & kEnd) != 0, fresh = (u.flags & (kFirst | kSecond)) != 0;
+        float ve[kHalves] = {};
+        bool there[kHalves] = {}, moves = false;
         if (ok && !end) {
-            if (u.flags & kFirst) {
-                ok = mbar_wait_warp<false>(bars.q_ready(item.i), item.phase, wc);
+            if (fresh) {
+                const int q = u.item & 1;
+                ok = mbar_wait_warp<false>(bars.q_ready(q), (uint32_t)(u.item >> 1) & 1u, wc);
 #pragma unroll
                 for (int h = 0; h < HP; ++h) {
-                    qs[h] = reinterpret_cast<const float *>(smem + C::kQs)[item.i * 16 + h];
+                    qs[h] = reinterpret_cast<const float *>(smem + C::kQs)[q * 16 + h];
                     m[h] = -INFINITY;
                     l[h] = 0.f;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bars.q_free(item.i));
-                item.next();
+                if (lane == 0) {
+                    mbar_arrive(bars.q_free(q));
+                    // (the other group has no part in an item of one unit)
+                    if ((u.flags & kFirst) && (u.flags & kLast)) mbar_arrive(bars.q_free(q));
+                }
             }
             ok = ok && mbar_wait_warp<false>(bars.s_full(buf.i), buf.phase, wc);
         }
         if (ok && !end) {
-            const uint8_t *ex = smem + C::kExp + get.i * 256 + r;
-            const float kf = __uint_as_float((uint32_t)ex[0] << 23);
-            ve = (float)ex[128] - 127.f;
-            there = r < u.rows && !((u.missing >> (r >> p.log2_page)) & 1u);
             tc_fence_after();
-            uint32_t raw[C::N1];
-            tmem_read(trow + 32u * buf.i, raw);
+#pragma unroll
+            for (int k = 0; k < kHalves; ++k) {
+                const int row = k * 128 + r;
+                const uint8_t *ex = smem + C::kExp + get.i * 2 * kUnit + row;
+                const float kf = __uint_as_float((uint32_t)ex[0] << 23);
+                ve[k] = (float)ex[kUnit] - 127.f;
+                there[k] = row < u.rows && !((u.missing >> (row >> log2_box)) & 1u);
+                uint32_t raw[C::N1];
+                tmem_read(trow + C::s_col(buf.i) + 32u * k, raw);
+                // scores in log2 units
+#pragma unroll
+                for (int h = 0; h < HP; ++h) {
+                    const float x =
+                        fmaf(__uint_as_float(raw[HP + h]), 0.03125f, __uint_as_float(raw[h]));
+                    s[k][h] = there[k] ? x * (qs[h] * kf) : -INFINITY;
+                    moves |= s[k][h] + ve[k] > m[h] + 1.f;
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.s_free(buf.i));
-            // scores in log2 units
-#pragma unroll
-            for (int h = 0; h < HP; ++h) {
-                const float x = fmaf(__uint_as_float(raw[HP + h]), 0.03125f, __uint_as_float(raw[h]));
-                s[h] = there ? x * (qs[h] * kf) : -INFINITY;
-                moves |= s[h] + ve > m[h] + 1.f;
-            }
         }
-        if (bar_any(1, 128, moves || !ok)) {
-            if (bar_any(1, 128, !ok)) return;
+        // P and O are free, and O whole, once the product of the group's unit before is done
+        ok = ok && mbar_wait_warp<false>(bars.pv_done(w), turn.phase ^ 1u, wc);
+        if (bar_any(1 + w, 128, moves || !ok)) {
+            if (bar_any(1 + w, 128, !ok)) return;
             if (!end) {
                 float f[HP];
 #pragma unroll
                 for (int h = 0; h < HP; ++h) {
-                    const float top = warp_max(s[h] + ve);
+                    float top = s[0][h] + ve[0];
+#pragma unroll
+                    for (int k = 1; k < kHalves; ++k) top = fmaxf(top, s[k][h] + ve[k]);
+                    top = warp_max(top);
                     if (lane == 0) red[warp * 16 + h] = top;
                 }
-                bar_softmax();
+                bar_group(w);
 #pragma unroll
                 for (int h = 0; h < HP; ++h) {
                     float mn = m[h];
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) mn = fmaxf(mn, red[w * 16 + h]);
+                    for (int k = 0; k < 4; ++k) mn = fmaxf(mn, red[k * 16 + h]);
                     f[h] = mn == -INFINITY ? 0.f : exp2_fast(m[h] - mn);
                     m[h] = mn;
                     l[h] *= f[h];
                 }
-                if (!(u.flags & kFirst)) {
-                    // O is whole once the product of the unit before is done
-                    ok = mbar_wait_warp<false>(bars.pv_done(buf.i ^ 1),
-                                               buf.i ? buf.phase : buf.phase ^ 1u, wc);
+                if (!fresh) {
                     tc_fence_after();
                     uint32_t o[C::N2];
-                    tmem_read(trow + C::kTmemO, o);
+                    tmem_read(to, o);
 #pragma unroll
                     for (int c = 0; c < C::N2; ++c)
                         if (c < 3 * HP) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c % HP]);
 #pragma unroll
-                    for (int c = 0; c < C::N2; c += 16)
-                        tmem_st16_async(trow + C::kTmemO + c, o + c);
+                    for (int c = 0; c < C::N2; c += 16) tmem_st16_async(to + c, o + c);
                     tmem_st_wait();
                     tc_fence_before();
                 }
             }
         }
         if (end) return;
-        // weights, times 2^7, as three terms; P's buffer is free once the product of
-        // the unit before the last is done
-        ok = ok && mbar_wait_warp<false>(bars.pv_done(buf.i), buf.phase ^ 1u, wc);
-        uint8_t *pb = smem + C::kP + buf.i * C::kPBytes;
+        // weights, times 2^7, as three terms
 #pragma unroll
-        for (int h = 0; h < HP; h += 2) {
-            float x[2];
+        for (int k = 0; k < kHalves; ++k) {
+            uint8_t *pb = smem + C::kP + (w * kHalves + k) * C::kPBytes;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float ms = m[h + c] == -INFINITY ? 0.f : m[h + c];
-                const float y = s[h + c] - ms;
-                l[h + c] += exp2_fast(y);
-                x[c] = exp2_fast(y + (ve + 7.f));
-            }
+            for (int h = 0; h < HP; h += 2) {
+                float x[2];
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const uint32_t a = f32x2_to_e4m3x2(x[0], x[1]);
-                pb[(k * HP + h) / 8 * 1024 + place[(k * HP + h) & 7]] = (uint8_t)a;
-                pb[(k * HP + h) / 8 * 1024 + place[(k * HP + h + 1) & 7]] = (uint8_t)(a >> 8);
-                if (k < 2) {
-                    const float2 y = e4m3x2_to_f32(a);
-                    x[0] = 16.f * (x[0] - y.x);
-                    x[1] = 16.f * (x[1] - y.y);
+                for (int c = 0; c < 2; ++c) {
+                    const float ms = m[h + c] == -INFINITY ? 0.f : m[h + c];
+                    const float y = s[k][h + c] - ms;
+                    l[h + c] += exp2_fast(y);
+                    x[c] = exp2_fast(y + (ve[k] + 7.f));
+                }
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    const uint32_t a = f32x2_to_e4m3x2(x[0], x[1]);
+                    const int n = t * HP + h;
+                    pb[n / 8 * 1024 + place[n & 7]] = (uint8_t)a;
+                    pb[n / 8 * 1024 + place[(n + 1) & 7]] = (uint8_t)(a >> 8);
+                    if (t < 2) {
+                        const float2 y = e4m3x2_to_f32(a);
+                        x[0] = 16.f * (x[0] - y.x);
+                        x[1] = 16.f * (x[1] - y.y);
+                    }
                 }
             }
         }
-        if (!there) {  // what lies in a row that does not count may be anything
-            uint4 *v = reinterpret_cast<uint4 *>(smem + get.i * 2 * kTileBytes + kTileBytes + r * 128);
+        if (u.rows < kUnit || u.missing) {  // (the values have to be there)
+            ok = ok && mbar_wait_warp<false>(bars.v_full(get.i), get.phase, wc);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < kHalves; ++k) {
+                if (!ok || there[k]) continue;  // what lies in other rows may be anything
+                uint4 *v = reinterpret_cast<uint4 *>(smem + C::kV + get.i * kTileBytes +
+                                                     (k * 128 + r) * 128);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
         fence_proxy_async_smem();  // P and V are read by the tensor core (async proxy)
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.p_full(buf.i));
-        if (u.flags & kLast) {
+        if (lane == 0) mbar_arrive(bars.p_full(w));
+        if (u.flags & (kLast | kLastBut1)) {
+            // the group's last unit of the item
+            float sum[HP];
 #pragma unroll
             for (int h = 0; h < HP; ++h) {
-                float t = l[h];
+                sum[h] = l[h];
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-                if (lane == 0) red[64 + warp * 16 + h] = t;
+                for (int off = 16; off > 0; off >>= 1)
+                    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], off);
+                if (lane == 0) red[64 + warp * 16 + h] = sum[h];
             }
-            ok = ok && mbar_wait_warp<false>(bars.pv_done(buf.i), buf.phase, wc);
+            ok = ok && mbar_wait_warp<false>(bars.pv_done(w), turn.phase, wc);
             tc_fence_after();
             uint32_t o[C::N2];
-            tmem_read(trow + C::kTmemO, o);
+            tmem_read(to, o);
             tc_fence_before();
-            bar_softmax();
+            bar_group(w);
+            float x[HP];
 #pragma unroll
             for (int h = 0; h < HP; ++h) {
-                if (h >= u.heads || !ok) break;
-                float sum = 0.f;
+                sum[h] = 0.f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) sum += red[64 + w * 16 + h];
-                const float x = 0.0078125f *
-                                fmaf(fmaf(__uint_as_float(o[2 * HP + h]), 0.0625f,
-                                          __uint_as_float(o[HP + h])),
-                                     0.0625f, __uint_as_float(o[h]));
-                if (u.flags & kWhole) {
-                    p.out[(int64_t)u.b * p.out_stride + (int64_t)(u.head0 + h) * 128 + r] =
-                        __float2bfloat16(sum > 0.f || sum != sum ? x / sum : 0.f);
-                } else {
-                    p.part_o[(int64_t)(u.slot + h) * 128 + r] = x;
-                    if (r == 0) p.part_ml[u.slot + h] = make_float2(m[h], sum);
+                for (int k = 0; k < 4; ++k) sum[h] += red[64 + k * 16 + h];
+                x[h] = 0.0078125f * fmaf(fmaf(__uint_as_float(o[2 * HP + h]), 0.0625f,
+                                              __uint_as_float(o[HP + h])),
+                                         0.0625f, __uint_as_float(o[h]));
+            }
+            if (u.flags & kLastBut1) {  // the other group has the item's last
+                ok = ok && mbar_wait_warp<false>(bars.join_free(), joins.phase ^ 1u, wc);
+                if (ok) {
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) {
+                        join[h * 130 + r] = x[h];
+                        if (r == 0) {
+                            join[h * 130 + 128] = m[h];
+                            join[h * 130 + 129] = sum[h];
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.join_full());
+                joins.next();
+            } else {
+                if (!(u.flags & kFirst)) {
+                    ok = ok && mbar_wait_warp<false>(bars.join_full(), joins.phase, wc);
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) {
+                        const float m1 = join[h * 130 + 128], mn = fmaxf(m[h], m1);
+                        const float f0 = m[h] == -INFINITY ? 0.f : exp2_fast(m[h] - mn);
+                        const float f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - mn);
+                        x[h] = x[h] * f0 + join[h * 130 + r] * f1;
+                        sum[h] = sum[h] * f0 + join[h * 130 + 129] * f1;
+                        m[h] = mn;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.join_free());
+                    joins.next();
+                }
+#pragma unroll
+                for (int h = 0; h < HP; ++h) {
+                    if (h >= u.heads || !ok) break;
+                    if (u.flags & kWhole) {
+                        p.out[(int64_t)u.b * p.out_stride + (int64_t)(u.head0 + h) * 128 + r] =
+                            __float2bfloat16(sum[h] > 0.f || sum[h] != sum[h] ? x[h] / sum[h] : 0.f);
+                    } else {
+                        p.part_o[(int64_t)(u.slot + h) * 128 + r] = x[h];
+                        if (r == 0) p.part_ml[u.slot + h] = make_float2(m[h], sum[h]);
+                    }
                 }
             }
-            bar_softmax();  // the sums are read
         }
-        buf.next();
-        get.next();
+        buf.next(2);
+        get.next(2);
+        turn.next();
     }
 }
 
@@ -547,30 +736,41 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ 
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5;
-    const Bars bars{smem_u32(smem) + C::kBars};
+    const Bars<HP> bars{smem_u32(smem) + C::kBars};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kSlots + 4);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(bars.full(s), 1);
-            mbar_init(bars.empty(s), 1);
+        for (int s = 0; s < C::kKeys; ++s) {
+            mbar_init(bars.k_full(s), 1);
+            mbar_init(bars.k_empty(s), 1);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bars.v_full(s), 1);
+            mbar_init(bars.v_empty(s), 1);
+            mbar_init(bars.posted(s), 1);
+            mbar_init(bars.told(s), 1 + 32);  // what the unit is, and 32 lanes' copies of scales
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.q_ready(i), 1);
-            mbar_init(bars.q_free(i), 5);  // the MMAs that read it, and four warps
-            mbar_init(bars.s_full(i), 1);
-            mbar_init(bars.s_free(i), 4);
+            mbar_init(bars.q_free(i), 9);  // the MMAs that read it, and eight warps
             mbar_init(bars.p_full(i), 4);
             mbar_init(bars.pv_done(i), 1);
         }
-        mbar_init(bars.drain(), 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bars.s_full(i), 1);
+            mbar_init(bars.s_free(i), 4);
+        }
+        mbar_init(bars.join_full(), 4);
+        mbar_init(bars.join_free(), 4);
+        mbar_init(bars.drain(0), 1);
+        mbar_init(bars.drain(1), 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&mK);
         tma_prefetch_desc(&mV);
     }
-    if (warp == 5) {
-        tmem_alloc(smem_u32(tmem_slot), 128u);
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512u);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -579,25 +779,30 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ 
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{p.wait_ns, p.err, abort_flag, 0u};
     griddep_wait();
-    if (warp < 4) {
-        softmax<HP>(p, smem, tmem, bars, wc);
-    } else if (warp == 4) {
-        feed<HP>(&mK, &mV, p, log2_box, smem, bars, wc);
+    if (warp < 8) {
+        softmax<HP>(p, warp >> 2, smem, tmem, bars, wc);
+    } else if (warp == 8) {
+        feed<HP>(&mK, p, log2_box, smem, bars, wc);
+    } else if (warp == 11) {
+        feed_values<HP>(&mV, p, log2_box, smem, bars, wc);
     } else if ((threadIdx.x & 31) == 0) {
-        issue<HP>(smem, tmem, bars, wc);
+        if (warp == 9)
+            issue_scores<HP>(smem, tmem, bars, wc);
+        else
+            issue_products<HP>(smem, tmem, bars, wc);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_dealloc(tmem, 128u);
+    if (warp == 9) tmem_dealloc(tmem, 512u);
 }
 
 template <int HP>
 cudaError_t launch(PagedArgs &a, const KvCacheSpec &cache, const LaunchCtx &ctx) {
     using C = Cfg<HP>;
     static_assert(C::kSmem <= 227 * 1024, "shared memory");
-    static_assert(C::N1 <= 32 && C::kTmemO + C::N2 <= 128, "TMEM");
+    static_assert(C::N1 <= 32 && C::N2 <= 48, "TMEM");
     const int log2_box = std::min(cache.log2_page, 7);
     CUtensorMap mK, mV;
     const cuuint64_t rows = (cuuint64_t)cache.H << cache.log2_page;
@@ -619,12 +824,8 @@ cudaError_t launch(PagedArgs &a, const KvCacheSpec &cache, const LaunchCtx &ctx)
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    const bool takes = paged_ways(a, kUnit, std::min(kMaxWays, ctx.num_sms));
-    count_launches(takes ? 3 : 2);
-    if (takes) {
-        e = launch_paged_begin(a, ctx);
-        if (e != cudaSuccess) return e;
-    }
+    a.ways = paged_ways(a, kUnit, std::min(kMaxWays, ctx.num_sms));
+    count_launches(1);
     return launch_pdl(paged_tc_kernel<HP>, dim3((unsigned)a.ways), dim3(kThreads), C::kSmem, ctx,
                       mK, mV, a, log2_box);
 }

@@ -213,8 +213,9 @@ wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
     if (!(scale > 0.f) || !(scale < INFINITY)) return WANVAE_ERR_INVALID_ARG;
     const size_t need = wanvae_paged_attention_workspace_size(n_heads, s.H, s.D);
     if (need == 0) return WANVAE_ERR_UNSUPPORTED;
-    // the units of 16 rows that the page table could hold are counted in 32 bits
-    const int64_t units = ((max_pages << s.log2_page) + 15) / 16;
+    // units of 16 rows that the page table could hold, and one more an item, are
+    // counted in 32 bits
+    const int64_t units = ((max_pages << s.log2_page) + 15) / 16 + 1;
     if (units > INT32_MAX / 64 || units * n_seq > INT32_MAX / n_heads) return WANVAE_ERR_UNSUPPORTED;
     const int64_t w = n_heads * s.D;
     if (!stride_ok(q_stride, w) || !stride_ok(out_stride, w)) return WANVAE_ERR_INVALID_ARG;
