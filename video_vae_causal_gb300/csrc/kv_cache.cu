@@ -16,8 +16,9 @@
 // contiguous, which is how attention over the cache reads them.  Both passes
 // move each row once (2 D bytes on one side, D + 1 on the other) and are bound
 // by HBM.  A row takes D / 8 lanes with one 16-byte vector of bf16 each; a
-// warp keeps the rows of a token's heads together, so that the token's
-// sequence and page are looked up once for all of them.
+// warp keeps the rows of a token's heads together and takes tokens in a row, so
+// that a token's page is looked up once for all heads and its sequence once for the
+// tokens that follow it.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -31,6 +32,8 @@ namespace wanvae {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFlight = 8;  // rows of a lane's that are loaded before the first is used
+constexpr int kBlocks = 3;  // resident blocks that leave the registers for them
 constexpr int kExpMin = -100, kExpMax = 120;
 
 struct CacheArgs {
@@ -52,42 +55,49 @@ __device__ __forceinline__ int64_t cache_row(const CacheArgs &c, int seq, int po
     return (((int64_t)page * c.H) << c.log2_page) + (pos & ((1 << c.log2_page) - 1));
 }
 
-// The scale's exponent of a row whose largest finite magnitude is amax:
-// ceil(log2(amax / 448)), from amax's own bits (448 = 1.75 * 2^8).
-__device__ __forceinline__ int row_exponent(float amax) {
-    const uint32_t b = __float_as_uint(amax);
-    if (b == 0u) return 0;
-    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+// The scale's exponent of a row whose largest finite magnitude has the bf16 bits
+// amax: ceil(log2(amax / 448)) (448 = 1.75 * 2^8).
+__device__ __forceinline__ int row_exponent(uint32_t amax) {
+    if (amax == 0u) return 0;
+    const int e = (int)(amax >> 7) - 127 - 8 + ((amax & 0x7fu) > 0x60u ? 1 : 0);
     return min(max(e, kExpMin), kExpMax);
 }
 
-// 8 bf16 values -> e4m3 with the row's scale; kLanes lanes hold the row.
+// Largest of two pairs of 16-bit magnitudes over the kLanes lanes of a row.
 template <int kLanes>
-__device__ __forceinline__ uint2 quantise8(const uint4 &v, int &e) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[8];
-    uint32_t amax = 0;  // magnitudes compare as integers; only finite ones count
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = nact_lo(w[i]);
-        x[2 * i + 1] = nact_hi(w[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t m = __float_as_uint(x[i]) & 0x7fffffffu;
-        const bool finite = m < 0x7f800000u;
-        amax = max(amax, finite ? m : 0u);
-        x[i] = finite ? x[i] : __uint_as_float(0x7fc00000u);
-    }
+__device__ __forceinline__ uint32_t row_max(uint32_t m) {
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1)
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    e = row_exponent(__uint_as_float(amax));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+    return max(m & 0xffffu, m >> 16);
+}
+
+// 8 bf16 values -> e4m3 with the row's scale; kLanes lanes hold the row, the whole
+// warp takes part.  Magnitudes compare as integers, two at a time; infinities and
+// NaN, the largest of them, are looked for only where a row has any.
+template <int kLanes>
+__device__ __forceinline__ uint2 quantise8(const uint4 &v, int &e) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    uint32_t amax = row_max<kLanes>(m);
+    if (__any_sync(0xffffffffu, amax >= 0x7f80u)) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t bad = __vcmpgeu2(w[i] & 0x7fff7fffu, 0x7f807f80u);
+            m = __vmaxu2(m, w[i] & 0x7fff7fffu & ~bad);
+            w[i] = (w[i] & ~bad) | (bad & 0x7fc07fc0u);
+        }
+        amax = row_max<kLanes>(m);
+    }
+    e = row_exponent(amax);
     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
     uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = f32x2_to_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    for (int i = 0; i < 4; ++i) q[i] = f32x2_to_e4m3x2(nact_lo(w[i]) * inv, nact_hi(w[i]) * inv);
+    return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
 // 8 e4m3 values of a row -> bf16 (exact for scales that leave bf16's range alone).
@@ -106,49 +116,70 @@ __device__ __forceinline__ uint4 dequantise8(const uint2 &q, uint32_t code) {
 
 // Rows cu_new[s] .. of k and v to the last positions of sequence s.
 template <int D, bool kQuant>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocks)
 kv_append_kernel(const CacheArgs c, const __nv_bfloat16 *__restrict__ k, int64_t k_stride,
                  const __nv_bfloat16 *__restrict__ v, int64_t v_stride,
                  const int32_t *__restrict__ lens, const int32_t *__restrict__ cu_new, int n_seq,
-                 int total) {
+                 int total, int per_warp) {
     griddep_launch_dependents();
     griddep_wait();
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a warp holds
     const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
-    const int warps = (gridDim.x * kThreads) >> 5;
-    for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < total; t += warps) {
-        int seq = t, first = t, end = t + 1;
-        if (cu_new) {
+    const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int t1 = (int)min((int64_t)total, (id + 1) * per_warp);
+    int seq = 0, first = 0, end = 0, len = 0;
+    for (int t = (int)min(id * per_warp, (int64_t)total); t < t1; ++t) {
+        // the token's H key rows, then its H value rows, kFlight turns' loads at a time; the
+        // first are in flight while the token's place is looked up
+        const int64_t kt = t * k_stride, vt = t * v_stride;
+        uint4 x[kFlight];
+        auto load = [&](int r0) {
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int r = r0 + i * kRows;
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < 2 * c.H)
+                    x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                     r >= c.H ? v + vt + (r - c.H) * D : k + kt + r * D) +
+                                 sub);
+            }
+        };
+        load(grp);
+        if (!cu_new) {
+            seq = first = t;
+            end = t + 1;
+            len = __ldg(lens + seq);
+        } else if (t >= end) {
             seq = seq_of_row(cu_new, n_seq, t);
             first = __ldg(cu_new + seq);
             end = __ldg(cu_new + seq + 1);
+            len = __ldg(lens + seq);
         }
         if (t < first || t >= end) continue;  // a row behind the last sequence
-        const int64_t row0 = cache_row(c, seq, __ldg(lens + seq) - (end - t));
+        const int64_t row0 = cache_row(c, seq, len - (end - t));
         if (row0 < 0) {
             if (lane == 0) atomicOr(c.err, kDevErrAlign);
             continue;
         }
-        // the token's H key rows, then its H value rows
-        for (int r0 = 0; r0 < 2 * c.H; r0 += kRows) {
-            const int r = r0 + grp;
-            const bool there = r < 2 * c.H, is_v = r >= c.H;
-            const int h = is_v ? r - c.H : r;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (there)
-                x = __ldg(reinterpret_cast<const uint4 *>((is_v ? v + t * v_stride
-                                                                : k + t * k_stride) +
-                                                          h * D) + sub);
-            const int64_t row = row0 + ((int64_t)h << c.log2_page);
-            uint8_t *dst = (is_v ? c.v : c.k) + row * (kQuant ? D : 2 * D);
-            if (kQuant) {
-                int e;
-                const uint2 q = quantise8<kLanes>(x, e);
-                if (!there) continue;
-                reinterpret_cast<uint2 *>(dst)[sub] = q;
-                if (sub == 0) (is_v ? c.v_exp : c.k_exp)[row] = (uint8_t)(e + 127);
-            } else if (there) {
-                reinterpret_cast<uint4 *>(dst)[sub] = x;
+        for (int r0 = grp; r0 < 2 * c.H + grp; r0 += kFlight * kRows) {
+            if (r0 >= kFlight * kRows) load(r0);
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int r = r0 + i * kRows;
+                if (r - grp >= 2 * c.H) break;
+                const bool there = r < 2 * c.H, is_v = r >= c.H;
+                const int h = is_v ? r - c.H : r;
+                const int64_t row = row0 + ((int64_t)h << c.log2_page);
+                uint8_t *dst = (is_v ? c.v : c.k) + row * (kQuant ? D : 2 * D);
+                if (kQuant) {
+                    int e;
+                    const uint2 q = quantise8<kLanes>(x[i], e);
+                    if (!there) continue;
+                    reinterpret_cast<uint2 *>(dst)[sub] = q;
+                    if (sub == 0) (is_v ? c.v_exp : c.k_exp)[row] = (uint8_t)(e + 127);
+                } else if (there) {
+                    reinterpret_cast<uint4 *>(dst)[sub] = x[i];
+                }
             }
         }
     }
@@ -156,39 +187,57 @@ kv_append_kernel(const CacheArgs c, const __nv_bfloat16 *__restrict__ k, int64_t
 
 // Positions 0 .. of sequence s to rows cu[s] .. of k and v.
 template <int D, bool kQuant>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocks)
 kv_gather_kernel(const CacheArgs c, const int32_t *__restrict__ cu, int n_seq, int total,
-                 __nv_bfloat16 *__restrict__ k, int64_t k_stride, __nv_bfloat16 *__restrict__ v,
+                 int per_warp, __nv_bfloat16 *__restrict__ k, int64_t k_stride, __nv_bfloat16 *__restrict__ v,
                  int64_t v_stride) {
     griddep_launch_dependents();
     griddep_wait();
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
-    const int warps = (gridDim.x * kThreads) >> 5;
-    for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < total; t += warps) {
-        const int seq = seq_of_row(cu, n_seq, t);
-        const int first = __ldg(cu + seq);
-        if (t < first || t >= __ldg(cu + seq + 1)) continue;
+    const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int t1 = (int)min((int64_t)total, (id + 1) * per_warp);
+    int seq = 0, first = 0, end = 0;
+    for (int t = (int)min(id * per_warp, (int64_t)total); t < t1; ++t) {
+        if (t >= end) {
+            seq = seq_of_row(cu, n_seq, t);
+            first = __ldg(cu + seq);
+            end = __ldg(cu + seq + 1);
+        }
+        if (t < first || t >= end) continue;
         const int64_t row0 = cache_row(c, seq, t - first);
         if (row0 < 0) {
             if (lane == 0) atomicOr(c.err, kDevErrAlign);
             continue;
         }
-        for (int r0 = 0; r0 < 2 * c.H; r0 += kRows) {
-            const int r = r0 + grp;
-            if (r >= 2 * c.H) continue;
-            const bool is_v = r >= c.H;
-            const int h = is_v ? r - c.H : r;
-            const int64_t row = row0 + ((int64_t)h << c.log2_page);
-            const uint8_t *src = (is_v ? c.v : c.k) + row * (kQuant ? D : 2 * D);
-            uint4 x;
-            if (kQuant)
-                x = dequantise8(__ldg(reinterpret_cast<const uint2 *>(src) + sub),
-                                __ldg((is_v ? c.v_exp : c.k_exp) + row));
-            else
-                x = __ldg(reinterpret_cast<const uint4 *>(src) + sub);
-            reinterpret_cast<uint4 *>((is_v ? v + t * v_stride : k + t * k_stride) + h * D)[sub] =
-                x;
+        const int64_t kt = t * k_stride, vt = t * v_stride;
+        for (int r0 = grp; r0 < 2 * c.H; r0 += kFlight * kRows) {
+            uint4 x[kFlight];
+            uint32_t code[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int r = r0 + i * kRows;
+                if (r >= 2 * c.H) break;
+                const bool is_v = r >= c.H;
+                const int64_t row = row0 + ((int64_t)(is_v ? r - c.H : r) << c.log2_page);
+                const uint8_t *src = (is_v ? c.v : c.k) + row * (kQuant ? D : 2 * D);
+                if (kQuant) {
+                    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src) + sub);
+                    x[i].x = q.x;
+                    x[i].y = q.y;
+                    code[i] = __ldg((is_v ? c.v_exp : c.k_exp) + row);
+                } else {
+                    x[i] = __ldg(reinterpret_cast<const uint4 *>(src) + sub);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int r = r0 + i * kRows;
+                if (r >= 2 * c.H) break;
+                __nv_bfloat16 *dst = r >= c.H ? v + vt + (r - c.H) * D : k + kt + r * D;
+                reinterpret_cast<uint4 *>(dst)[sub] =
+                    kQuant ? dequantise8(make_uint2(x[i].x, x[i].y), code[i]) : x[i];
+            }
         }
     }
 }
@@ -209,9 +258,14 @@ CacheArgs cache_args(const KvCacheSpec &c, const int32_t *table, int max_pages,
     return a;
 }
 
-// One token a warp, at most 8 resident blocks a multiprocessor.
-unsigned grid_of(int total, const LaunchCtx &ctx) {
-    return (unsigned)std::min((total + kThreads / 32 - 1) / (kThreads / 32), ctx.num_sms * 8);
+// Tokens of a warp: one resident wave's share.
+int tokens_per_warp(int total, const LaunchCtx &ctx) {
+    const int warps = ctx.num_sms * kBlocks * (kThreads / 32);
+    return total / warps + (total % warps ? 1 : 0);
+}
+unsigned blocks_for(int total, int per_warp) {
+    const int warps = (total + per_warp - 1) / per_warp;
+    return (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
 }
 
 }  // namespace
@@ -223,10 +277,11 @@ cudaError_t launch_kv_append(const KvCacheSpec &c, const void *k, int64_t k_stri
     const CacheArgs a = cache_args(c, table, max_pages, ctx);
     auto *kp = static_cast<const __nv_bfloat16 *>(k);
     auto *vp = static_cast<const __nv_bfloat16 *>(v);
-    const dim3 grid(grid_of(total, ctx)), block(kThreads);
+    const int per_warp = tokens_per_warp(total, ctx);
+    const dim3 grid(blocks_for(total, per_warp)), block(kThreads);
     auto go = [&](auto kern) {
         return launch_pdl(kern, grid, block, 0, ctx, a, kp, k_stride, vp, v_stride, lens, cu_new,
-                          n_seq, total);
+                          n_seq, total, per_warp);
     };
     if (c.D == 64) return c.e4m3 ? go(kv_append_kernel<64, true>) : go(kv_append_kernel<64, false>);
     if (c.D == 128)
@@ -240,10 +295,11 @@ cudaError_t launch_kv_gather(const KvCacheSpec &c, const int32_t *table, int max
     const CacheArgs a = cache_args(c, table, max_pages, ctx);
     auto *kp = static_cast<__nv_bfloat16 *>(k);
     auto *vp = static_cast<__nv_bfloat16 *>(v);
-    const dim3 grid(grid_of(total, ctx)), block(kThreads);
+    const int per_warp = tokens_per_warp(total, ctx);
+    const dim3 grid(blocks_for(total, per_warp)), block(kThreads);
     auto go = [&](auto kern) {
-        return launch_pdl(kern, grid, block, 0, ctx, a, cu, n_seq, total, kp, k_stride, vp,
-                          v_stride);
+        return launch_pdl(kern, grid, block, 0, ctx, a, cu, n_seq, total, per_warp, kp, k_stride,
+                          vp, v_stride);
     };
     if (c.D == 64) return c.e4m3 ? go(kv_gather_kernel<64, true>) : go(kv_gather_kernel<64, false>);
     if (c.D == 128)
