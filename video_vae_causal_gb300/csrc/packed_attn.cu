@@ -224,17 +224,18 @@ __device__ void producer(const CUtensorMap *mQ, const CUtensorMap *mK, const CUt
     }
 }
 
-// MMA issuer (one thread).  Tile w takes part in blocks j < n[w].
+// MMA issuer (one warp).  Tile w takes part in blocks j < n[w].
 template <int D>
-__device__ void issuer(const int (&n)[2], int blocks, uint32_t sbase, uint32_t tmem,
-                       const Bars<D> &bars, const WaitCtl &wc) {
+__device__ void issuer(int n0, int n1, uint32_t sbase, uint32_t tmem, const Bars<D> &bars,
+                       const WaitCtl &wc) {
     using L = Layout<D>;
     const uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32_bt(128, D);
     const uint64_t q0 = sdesc_kmajor(sbase + L::kQ, 128u, kLayoutSw128);
     const uint64_t k0 = sdesc_kmajor(sbase + L::kRing, 128u, kLayoutSw128);
     const uint64_t v0 = sdesc_rows_sw128(sbase + L::kRing, kAtom);
     constexpr uint32_t kTile16 = L::kTile >> 4;
-    auto scores = [&](int w, int j) {  // S = Q K_j^T
+    const int blocks = max(n0, n1);
+    auto scores = [&](int w, int j) {  // S = Q K_j^T (in the elected lane)
         const uint64_t a = q0 + (uint32_t)w * kTile16;
         const uint64_t b = k0 + (uint32_t)(fill_k(j) % L::kStages) * kTile16;
 #pragma unroll
@@ -244,42 +245,56 @@ __device__ void issuer(const int (&n)[2], int blocks, uint32_t sbase, uint32_t t
         }
         mma_commit(bars.s_full(w));
     };
-    bool ok = mbar_wait<false>(bars.q_full(), 0u, wc) &&
-              mbar_wait<false>(bars.full(fill_k(0)), 0u, wc);
+    bool ok = mbar_wait_warp<false>(bars.q_full(), 0u, wc) &&
+              mbar_wait_warp<false>(bars.full(fill_k(0)), 0u, wc);
     if (ok) {
         tc_fence_after();
-        for (int w = 0; w < 2; ++w)
-            if (n[w] > 0) scores(w, 0);
-        mma_commit(bars.empty(fill_k(0)));
+        if (elect_one()) {
+            if (n0 > 0) scores(0, 0);
+            if (n1 > 0) scores(1, 0);
+            mma_commit(bars.empty(fill_k(0)));
+        }
+        __syncwarp();
     }
     for (int j = 0; ok && j < blocks; ++j) {
-        ok = mbar_wait<false>(bars.full(fill_v(j)), bars.phase(fill_v(j)), wc);
+        ok = mbar_wait_warp<false>(bars.full(fill_v(j)), bars.phase(fill_v(j)), wc);
         if (ok && j + 1 < blocks)
-            ok = mbar_wait<false>(bars.full(fill_k(j + 1)), bars.phase(fill_k(j + 1)), wc);
+            ok = mbar_wait_warp<false>(bars.full(fill_k(j + 1)), bars.phase(fill_k(j + 1)), wc);
         const uint64_t b = v0 + (uint32_t)(fill_v(j) % L::kStages) * kTile16;
-        for (int w = 0; ok && w < 2; ++w) {
-            if (j >= n[w]) continue;
-            ok = mbar_wait<false>(bars.p_full(w), (uint32_t)j & 1u, wc);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int n = w ? n1 : n0;
+            if (!ok || j >= n) continue;
+            ok = mbar_wait_warp<false>(bars.p_full(w), (uint32_t)j & 1u, wc);
             if (!ok) break;
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kRows / 16; ++kk)
-                mma_bf16_ts(tmem + L::kO + 128u * w, tmem + 128u * w + kk * 8, b + kk * (2048u >> 4),
-                            id_o, j > 0 || kk > 0);
-            if (j + 1 < n[w])
-                scores(w, j + 1);
-            else
-                mma_commit(bars.o_full(w));
+                for (int kk = 0; kk < kRows / 16; ++kk)
+                    mma_bf16_ts(tmem + L::kO + 128u * w, tmem + 128u * w + kk * 8,
+                                b + kk * (2048u >> 4), id_o, j > 0 || kk > 0);
+                if (j + 1 < n)
+                    scores(w, j + 1);
+                else
+                    mma_commit(bars.o_full(w));
+            }
+            __syncwarp();
         }
         if (!ok) break;
-        mma_commit(bars.empty(fill_v(j)));
-        if (j + 1 < blocks) mma_commit(bars.empty(fill_k(j + 1)));
+        if (elect_one()) {
+            mma_commit(bars.empty(fill_v(j)));
+            if (j + 1 < blocks) mma_commit(bars.empty(fill_k(j + 1)));
+        }
+        __syncwarp();
     }
     // Every MMA issued above completes before TMEM is released.
     volatile int no_abort = 0;
     const WaitCtl dc{kDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
-    mma_commit(bars.drain());
-    mbar_wait<false>(bars.drain(), 0u, dc);
+    if (elect_one()) {
+        mma_commit(bars.drain());
+        mbar_wait<false>(bars.drain(), 0u, dc);
+    }
+    __syncwarp();
 }
 
 // Softmax and epilogue of tile w (4 warps, one row a thread: the TMEM lane
@@ -379,7 +394,8 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bars.p_full(w));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.p_full(w));
     }
     if (nkb > 0) {
         if (!mbar_wait_warp<false>(bars.o_full(w), 0u, wc)) return;
@@ -435,7 +451,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const Bars<D> bars{sbase + L::kBars};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kBars + 240);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kBars + 244);
@@ -444,7 +460,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
         mbar_init(bars.drain(), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(bars.s_full(w), 1);
-            mbar_init(bars.p_full(w), 128);
+            mbar_init(bars.p_full(w), 4);
             mbar_init(bars.o_full(w), 1);
         }
         for (int s = 0; s < L::kStages; ++s) {
@@ -478,10 +494,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
             softmax<D>(p, tl, warp >> 2, kvh, n, blocks, keys_cta, smem, tmem, bars, wc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (lane == 0 && blocks > 0) {
-            if (warp == 8) issuer<D>(n, blocks, sbase, tmem, bars, wc);
-            if (warp == 9) producer<D>(&mQ, &mK, &mV, p, tl, kvh, blocks, sbase, bars, wc);
-        }
+        if (warp == 8 && blocks > 0)
+            issuer<D>(__shfl_sync(0xffffffffu, n[0], 0), __shfl_sync(0xffffffffu, n[1], 0), sbase,
+                      __shfl_sync(0xffffffffu, tmem, 0), bars, wc);
+        if (warp == 9 && lane == 0 && blocks > 0)
+            producer<D>(&mQ, &mK, &mV, p, tl, kvh, blocks, sbase, bars, wc);
     }
     __syncwarp();
     tc_fence_before();

@@ -92,6 +92,20 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp.  Work that a whole warp walks through, with only the
+// tensor-core instructions inside this branch, keeps their descriptors in uniform
+// registers; walked through by one lane alone they were moved there for every
+// instruction (about 130 cycles an MMA, four times what the MMA takes).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Two fp32 lanes in one instruction.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
     uint64_t r;
