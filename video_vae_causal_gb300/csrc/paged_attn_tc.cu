@@ -412,15 +412,18 @@ __device__ void feed_values(const CUtensorMap *mV, const PagedArgs &p, int log2_
     if (!ok && lane == 0) drain_loads(fills, bars, true, wc);
 }
 
-// Every MMA that this thread issued completes before TMEM is released.
+// Every MMA that this warp issued completes before TMEM is released.
 __device__ __forceinline__ void drain_mmas(uint32_t bar, const WaitCtl &wc) {
     volatile int no_abort = 0;
     const WaitCtl dc{kPagedDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
-    mma_commit(bar);
-    mbar_wait<false>(bar, 0u, dc);
+    if (elect_one()) {
+        mma_commit(bar);
+        mbar_wait<false>(bar, 0u, dc);
+    }
+    __syncwarp();
 }
 
-// Warp 9, one thread: the scores.
+// Warp 9: the scores.
 template <int HP>
 __device__ void issue_scores(uint8_t *smem, uint32_t tmem, const Bars<HP> &bars, const WaitCtl &wc) {
     using C = Cfg<HP>;
@@ -432,25 +435,29 @@ __device__ void issue_scores(uint8_t *smem, uint32_t tmem, const Bars<HP> &bars,
     Turn<C::kStages> get;
     Turn<C::kKeys> key;
     Turn<4> buf;
-    while (mbar_wait<false>(bars.k_full(key.i), key.phase, wc)) {
-        const int flags = queue[get.i].flags, item = queue[get.i].item;
+    while (mbar_wait_warp<false>(bars.k_full(key.i), key.phase, wc)) {
+        const int flags = __shfl_sync(0xffffffffu, queue[get.i].flags, 0);
+        const int item = __shfl_sync(0xffffffffu, queue[get.i].item, 0);
         if (flags & kEnd) break;
         if ((flags & kFirst) &&
-            !mbar_wait<false>(bars.q_ready(item & 1), (uint32_t)(item >> 1) & 1u, wc))
+            !mbar_wait_warp<false>(bars.q_ready(item & 1), (uint32_t)(item >> 1) & 1u, wc))
             break;
-        if (!mbar_wait<false>(bars.s_free(buf.i), buf.phase ^ 1u, wc)) break;
+        if (!mbar_wait_warp<false>(bars.s_free(buf.i), buf.phase ^ 1u, wc)) break;
         tc_fence_after();
-        const uint64_t a = k0 + (uint32_t)key.i * (kTileBytes >> 4);
-        const uint64_t b = q0 + (uint32_t)(item & 1) * (C::kQBytes >> 4);
+        if (elect_one()) {
+            const uint64_t a = k0 + (uint32_t)key.i * (kTileBytes >> 4);
+            const uint64_t b = q0 + (uint32_t)(item & 1) * (C::kQBytes >> 4);
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h)
+            for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_e4m3_ss(tmem + C::s_col(buf.i) + 32u * h, a + h * (kHalfBytes >> 4) + k * 2,
-                            b + k * 2, id, k > 0);
-        mma_commit(bars.s_full(buf.i));
-        mma_commit(bars.k_empty(key.i));
-        if (flags & kLast) mma_commit(bars.q_free(item & 1));
+                for (int k = 0; k < 4; ++k)
+                    mma_e4m3_ss(tmem + C::s_col(buf.i) + 32u * h, a + h * (kHalfBytes >> 4) + k * 2,
+                                b + k * 2, id, k > 0);
+            mma_commit(bars.s_full(buf.i));
+            mma_commit(bars.k_empty(key.i));
+            if (flags & kLast) mma_commit(bars.q_free(item & 1));
+        }
+        __syncwarp();
         buf.next();
         get.next();
         key.next();
@@ -458,7 +465,7 @@ __device__ void issue_scores(uint8_t *smem, uint32_t tmem, const Bars<HP> &bars,
     drain_mmas(bars.drain(0), wc);
 }
 
-// Warp 10, one thread: the products.
+// Warp 10: the products.
 template <int HP>
 __device__ void issue_products(uint8_t *smem, uint32_t tmem, const Bars<HP> &bars, const WaitCtl &wc) {
     using C = Cfg<HP>;
@@ -469,22 +476,25 @@ __device__ void issue_products(uint8_t *smem, uint32_t tmem, const Bars<HP> &bar
     const uint64_t p0 = sdesc_kmajor(sbase + C::kP, 128u, kLayoutSw128);
     Turn<C::kStages> get;
     Turn<2> w;
-    while (mbar_wait<false>(bars.v_full(get.i), get.phase, wc)) {
-        const int flags = queue[get.i].flags;
-        if ((flags & kEnd) || !mbar_wait<false>(bars.p_full(w.i), w.phase, wc)) break;
+    while (mbar_wait_warp<false>(bars.v_full(get.i), get.phase, wc)) {
+        const int flags = __shfl_sync(0xffffffffu, queue[get.i].flags, 0);
+        if ((flags & kEnd) || !mbar_wait_warp<false>(bars.p_full(w.i), w.phase, wc)) break;
         tc_fence_after();
-        const uint32_t more = (flags & (kFirst | kSecond)) ? 0u : 1u;
-        const uint64_t a = v0 + (uint32_t)get.i * (kTileBytes >> 4);
-        const uint64_t b = p0 + (uint32_t)w.i * (kHalves * C::kPBytes >> 4);
-        const uint32_t d = tmem + C::o_col(w.i);
+        if (elect_one()) {
+            const uint32_t more = (flags & (kFirst | kSecond)) ? 0u : 1u;
+            const uint64_t a = v0 + (uint32_t)get.i * (kTileBytes >> 4);
+            const uint64_t b = p0 + (uint32_t)w.i * (kHalves * C::kPBytes >> 4);
+            const uint32_t d = tmem + C::o_col(w.i);
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h)
+            for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_e4m3_ss(d, a + h * (kHalfBytes >> 4) + k * (32 * 128 >> 4),
-                            b + h * (C::kPBytes >> 4) + k * 2, id, h + k > 0 ? 1u : more);
-        mma_commit(bars.pv_done(w.i));
-        mma_commit(bars.v_empty(get.i));
+                for (int k = 0; k < 4; ++k)
+                    mma_e4m3_ss(d, a + h * (kHalfBytes >> 4) + k * (32 * 128 >> 4),
+                                b + h * (C::kPBytes >> 4) + k * 2, id, h + k > 0 ? 1u : more);
+            mma_commit(bars.pv_done(w.i));
+            mma_commit(bars.v_empty(get.i));
+        }
+        __syncwarp();
         w.next();
         get.next();
     }
@@ -735,7 +745,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ 
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     griddep_launch_dependents();
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const Bars<HP> bars{smem_u32(smem) + C::kBars};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kSlots + 4);
@@ -785,11 +795,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ 
         feed<HP>(&mK, p, log2_box, smem, bars, wc);
     } else if (warp == 11) {
         feed_values<HP>(&mV, p, log2_box, smem, bars, wc);
-    } else if ((threadIdx.x & 31) == 0) {
-        if (warp == 9)
-            issue_scores<HP>(smem, tmem, bars, wc);
-        else
-            issue_products<HP>(smem, tmem, bars, wc);
+    } else if (warp == 9) {
+        issue_scores<HP>(smem, __shfl_sync(0xffffffffu, tmem, 0), bars, wc);
+    } else {
+        issue_products<HP>(smem, __shfl_sync(0xffffffffu, tmem, 0), bars, wc);
     }
     __syncwarp();
     tc_fence_before();
