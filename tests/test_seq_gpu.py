@@ -182,6 +182,42 @@ def test_packed_causal_future_does_not_leak(cuda_lib, D, bad):
     close(got[:ok, 0], o, a, "before the first bad key")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [1, 2, 8])
+def test_packed_causal_values_not_finite(cuda_lib, D, group):
+    # infinities and NaN in single elements of values: the rows that see them, and no
+    # others, get them (of both signs: NaN), in those elements alone
+    n, hkv = 430, 2
+    g = gen(13)
+    q, k, v = (normal(g, n, h, D) for h in (hkv * group, hkv, hkv))
+    v[5, 0, 3] = math.inf
+    v[140, 0, 7], v[141, 0, 7], v[140, 0, 40] = math.inf, -math.inf, -math.inf
+    v[129, 1, D - 1] = math.nan
+    v[255:258, 1, 16] = -math.inf
+    v[n - 1, 0] = math.nan
+    v[n - 2, 1, 0] = math.inf
+    got = cuda_lib.packed_attention(q, k, v, starts([n]))
+    cuda_lib.sync_status()
+    for h in range(hkv * group):
+        o, a = attend(q[:, h], k[:, h // group], v[:, h // group], causal_mask(n, n), D ** -0.5)
+        x, fin = got[:, h].double(), torch.isfinite(o)
+        assert torch.equal(torch.isnan(x), torch.isnan(o))
+        assert torch.equal(x[torch.isinf(o)], o[torch.isinf(o)])
+        close(torch.where(fin, x, 0.0), torch.where(fin, o, 0.0), torch.where(fin, a, 0.0))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_packed_values_all_nan(cuda_lib, causal):
+    # every value is NaN: every row that sees a key is NaN, one that sees none is zero
+    g = gen(14)
+    q, k = normal(g, 300, 4, 64), normal(g, 260, 1, 64)
+    v = torch.full_like(k, math.nan)
+    got = cuda_lib.packed_attention(q, k, v, starts([300]), starts([260]), causal=causal)
+    cuda_lib.sync_status()
+    first = 40 if causal else 0
+    assert torch.isnan(got[first:]).all() and (got[:first] == 0).all()
+
+
 def test_packed_lowest_value_rows(cuda_lib):
     # keys of the type's lowest value give scores of -inf and +inf's neighbours
     # where they are seen, and nothing where they are masked
@@ -227,6 +263,29 @@ def test_packed_timeout_reports_and_context_survives(cuda_lib):
     cuda_lib.sync_status()
     o, a = attend_clean(q[:, 1], k[:, 1], v[:, 1], causal_mask(300, 300), 128 ** -0.5)
     close(got[:, 1], o, a)
+
+
+def test_packed_graph_and_other_stream(cuda_lib):
+    g = gen(15)
+    qkv = normal(g, 400, 6, 128)
+    cu = starts([150, 250])
+    want = cuda_lib.packed_attention(qkv[:, :4], qkv[:, 4:5], qkv[:, 5:], cu)
+    cuda_lib.sync_status()
+    src, out = torch.zeros_like(qkv), torch.empty_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        cuda_lib.packed_attention(src[:, :4], src[:, 4:5], src[:, 5:], cu, out=out)
+        y, _ = cuda_lib.gated_residual_norm(out, want)
+    src.copy_(qkv)
+    graph.replay()
+    torch.cuda.synchronize()
+    cuda_lib.sync_status()
+    assert torch.equal(out, want) and torch.equal(y, want + want)
+    got = cuda_lib.packed_attention(qkv[:, :4], qkv[:, 4:5], qkv[:, 5:], cu, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
 
 
 # ------------------------------------------------------------------ the cache
@@ -470,6 +529,148 @@ def test_paged_behind_the_length_does_not_leak(cuda_lib):
             o, a = attend_clean(q[s:s + 1, h], k[:, 0], v[:, 0],
                                 torch.ones((1, n), dtype=torch.bool, device=DEV), 0.125)
             close(got[s:s + 1, h], o, a)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page", [16, 32, 128, 256, 1024])
+def test_paged_behind_the_length_and_bad_pages(cuda_lib, dtype, page):
+    """D = 128: what lies behind the length is not finite (scales too); then a page that
+    is not there, a negative length and one beyond the page table: the rest is attended."""
+    full, lens, D, group = [2 * page, 1040 + page, 5 * page], [page + 3, 1037, 4 * page + 1], 128, 4
+    cache, table, _, _ = fill(cuda_lib, full, page, 1, D, dtype, seed=page)
+    kept = [rows_of(cache, table, s, n) for s, n in enumerate(full)]
+    for s, n in enumerate(lens):
+        pos = torch.arange(n, full[s], device=DEV)
+        at = table[s].long()[pos // page]
+        for x, bad in ((cache.k, math.nan), (cache.v, math.nan)):
+            if dtype == torch.bfloat16:
+                x[at, :, pos % page] = bad
+            else:
+                x.view(torch.uint8)[at, :, pos % page] = 0x7f
+        for e in (cache.k_exp, cache.v_exp):
+            if e is not None:
+                e.view(torch.uint8)[at, :, pos % page] = 255
+    q = normal(gen(9), 3, group, D)
+
+    def check(got, seen):
+        for s, (k, v) in enumerate(kept):
+            see = torch.zeros((1, k.shape[0]), dtype=torch.bool, device=DEV)
+            see[0, seen[s]] = True
+            for h in range(group):
+                o, a = attend(q[s:s + 1, h], k[:, 0], v[:, 0], see, D ** -0.5)
+                close(got[s:s + 1, h], o, a, f"sequence {s}, head {h}")
+    got = cuda_lib.paged_attention(q, cache, ints(lens), table)
+    cuda_lib.sync_status()
+    check(got, [torch.arange(n, device=DEV) for n in lens])
+    broken = table.clone()
+    broken[0, 0] = -1
+    broken[2, 1] = cache.k.shape[0]
+    got = cuda_lib.paged_attention(q, cache, ints([lens[0], -5, lens[2]]), broken)
+    with pytest.raises(cuda_lib.WanvaeError):
+        cuda_lib.sync_status()
+    rest = torch.arange(lens[2], device=DEV)
+    check(got, [torch.arange(page, lens[0], device=DEV), torch.arange(0, device=DEV),
+                rest[rest // page != 1]])
+    narrow = table[:, :1].contiguous()
+    got = cuda_lib.paged_attention(q, cache, ints([page, page + 1, 2 ** 31 - 1]), narrow)
+    with pytest.raises(cuda_lib.WanvaeError):
+        cuda_lib.sync_status()
+    check(got, [torch.arange(page, device=DEV)] * 3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [33, 700])
+def test_paged_many_sequences_share_pages(cuda_lib, dtype, D, n):
+    """Many short sequences, all of them over the same pages: more items than CTAs."""
+    page, group = 16, 2
+    cache, table, _, _ = fill(cuda_lib, [70], page, 2, D, dtype, seed=n)
+    lens = [(7 * i) % 71 for i in range(n)]
+    q = normal(gen(n), n, 2 * group, D)
+    got = cuda_lib.paged_attention(q, cache, ints(lens), table.expand(n, -1).contiguous())
+    cuda_lib.sync_status()
+    k, v = rows_of(cache, table, 0, 70)
+    see = torch.arange(70, device=DEV)[None] < torch.tensor(lens, device=DEV)[:, None]
+    for h in range(2 * group):
+        o, a = attend_clean(q[:, h], k[:, h // group], v[:, h // group], see, D ** -0.5)
+        close(got[:, h], o, a, f"head {h}")
+    kk, vv = cuda_lib.kv_cache_gather(cache, table.expand(n, -1).contiguous(), starts(lens),
+                                      total=sum(lens))
+    cuda_lib.sync_status()
+    at = torch.cat([torch.arange(x, device=DEV) for x in lens])
+    assert torch.equal(kk.double(), k[at]) and torch.equal(vv.double(), v[at])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_paged_query_not_finite(cuda_lib, dtype, bad):
+    """One head's query is not finite: that head's row is NaN, no other's."""
+    cache, table, _, _ = fill(cuda_lib, [300, 40], 32, 2, 128, dtype, seed=4)
+    q = normal(gen(5), 2, 8, 128)
+    clean = cuda_lib.paged_attention(q, cache, ints([300, 40]), table)
+    q[0, 3, 17] = bad
+    got = cuda_lib.paged_attention(q, cache, ints([300, 40]), table)
+    cuda_lib.sync_status()
+    assert torch.isnan(got[0, 3]).all()
+    keep = torch.ones((2, 8), dtype=torch.bool, device=DEV)
+    keep[0, 3] = False
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.float8_e4m3fn, 128), (torch.float8_e4m3fn, 64),
+                                     (torch.bfloat16, 128)])
+def test_paged_timeout_reports_and_context_survives(cuda_lib, dtype, D):
+    lens = [3000, 17, 600]
+    cache, table, _, _ = fill(cuda_lib, lens, 64, 2, D, dtype, seed=6)
+    q = normal(gen(6), 3, 8, D)
+    want = cuda_lib.paged_attention(q, cache, ints(lens), table)
+    cuda_lib.sync_status()
+    try:
+        cuda_lib.set_wait_limit_ns(0)
+        cuda_lib.paged_attention(q, cache, ints(lens), table)
+        with pytest.raises(cuda_lib.WanvaeError) as ei:
+            cuda_lib.sync_status()
+        assert ei.value.status == cuda_lib.ERR_TIMEOUT
+    finally:
+        cuda_lib.set_wait_limit_ns(10 ** 9)
+    got = cuda_lib.paged_attention(q, cache, ints(lens), table)
+    cuda_lib.sync_status()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_paged_two_streams_at_once(cuda_lib, dtype):
+    """Two calls at once, each with its own workspace, and a graph of each replayed on
+    two streams: the results of calls one after another."""
+    lens = [9000, 4000, 30]
+    cache, table, _, _ = fill(cuda_lib, lens, 64, 2, 128, dtype, seed=8)
+    qs = [normal(gen(i), 3, 8, 128) for i in range(2)]
+    at = [ints(lens), ints([n // 2 for n in lens])]
+    want = [cuda_lib.paged_attention(qs[i], cache, at[i], table) for i in range(2)]
+    outs = [torch.empty_like(w) for w in want]
+    ws = [cuda_lib.make_paged_attention_workspace(qs[i], cache) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            cuda_lib.paged_attention(qs[i], cache, at[i], table, out=outs[i], workspace=ws[i])
+    for eager in (True, False):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i in range(2):
+                if eager:
+                    cuda_lib.paged_attention(qs[i], cache, at[i], table, out=outs[i],
+                                             workspace=ws[i], stream=streams[i])
+                else:
+                    with torch.cuda.stream(streams[i]):
+                        graphs[i].replay()
+        torch.cuda.synchronize()
+        cuda_lib.sync_status()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
 # ------------------------------------------------------------------ gated residual and norms

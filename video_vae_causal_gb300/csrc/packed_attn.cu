@@ -27,10 +27,10 @@
 // D = 64 the MMAs halve and the exponentials do not.
 //
 // Masked scores are replaced, never added to, so nothing in a masked key
-// reaches a row.  A masked value's weight is zero, but 0 * NaN is not: the value
-// rows behind the last key that the tile sees are zeroed in shared memory, and a
-// causal row that comes out non-finite is computed again over the keys that it
-// sees, key by key (only non-finite inputs lead there).
+// reaches a row.  A masked value's weight is zero, but 0 * NaN is not: of the blocks
+// that some row of the CTA sees in part (the last three at most) the value rows
+// behind the last key are zeroed in shared memory, and so are elements that are
+// not finite; those are added afterwards to the rows that see them, key by key.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -153,36 +153,86 @@ __device__ Tile find_tile(const PackedArgs &p, int x) {
     return r;
 }
 
-// A row that met a non-finite value, over the keys that it sees alone; whole
-// warp, lane l holds outputs l * D / 32 ...
+// The bf16 pairs of w that are not finite, as masks of 16 bits.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u);
+}
+
+// A value row of a block in shared memory (row `row` of 128, the blocks of 64
+// elements kAtom apart): zeros where `behind`, else without its elements that are
+// not finite; true where it had any.  The row's 16-byte pieces are taken in any
+// order (the swizzle stays within a row), a different one by each of eight lanes.
 template <int D>
-__device__ __noinline__ void slow_row(const PackedArgs &p, int q, int head, int kvh, int k0,
-                                      int keys) {
+__device__ __forceinline__ bool clean_row(uint8_t *block, int row, bool behind) {
+    uint32_t m = 0;
+    uint4 *v = reinterpret_cast<uint4 *>(block) + row * 8;
+#pragma unroll
+    for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint4 *at = v + a * (kAtom / 16) + (c ^ (row & 7));
+            if (behind) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            const uint4 x = *at;
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        }
+    if (!not_finite(m)) return false;
+    for (int a = 0; a < D / 64; ++a)
+        for (int c = 0; c < 8; ++c) {
+            uint4 x = v[a * (kAtom / 16) + c];
+            x.x &= ~not_finite(x.x);
+            x.y &= ~not_finite(x.y);
+            x.z &= ~not_finite(x.z);
+            x.w &= ~not_finite(x.w);
+            v[a * (kAtom / 16) + c] = x;
+        }
+    return true;
+}
+
+// Adds to a row that is written the value elements that clean_row took out of the keys
+// [from, keys) (they are not finite, so their sum is the output, whatever l is); m:
+// the row's maximum in log2 units.  Whole warp, lane l holds outputs l * D / 32 ..
+template <int D>
+__device__ __noinline__ void put_back(const PackedArgs &p, int q, int head, int kvh, int k0,
+                                      int from, int keys, float m) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const __nv_bfloat16 *qr = p.q + (int64_t)q * p.q_stride + (int64_t)head * D + lane * E;
-    float qv[E], o[E] = {}, m = -INFINITY, l = 0.f;
+    float qv[E], o[E] = {};
 #pragma unroll
     for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(qr[e]);
-    for (int j = 0; j < keys; ++j) {
-        const __nv_bfloat16 *kr = p.k + (int64_t)(k0 + j) * p.k_stride + (int64_t)kvh * D + lane * E;
-        const __nv_bfloat16 *vr = p.v + (int64_t)(k0 + j) * p.v_stride + (int64_t)kvh * D + lane * E;
+    bool any = false;
+    for (int j = from; j < keys; ++j) {
+        const int64_t at = (int64_t)kvh * D + lane * E;
+        const __nv_bfloat16 *vr = p.v + (int64_t)(k0 + j) * p.v_stride + at;
+        float v[E];
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            v[e] = __bfloat162float(vr[e]);
+            bad |= !isfinite(v[e]);
+        }
+        if (!__any_sync(0xffffffffu, bad)) continue;
+        const __nv_bfloat16 *kr = p.k + (int64_t)(k0 + j) * p.k_stride + at;
         float s = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) s = fmaf(qv[e], __bfloat162float(kr[e]), s);
         s = nact_group_sum(s, 32) * p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float w = mn == -INFINITY ? 0.f : exp2f(s - mn);
-        m = mn;
-        l = l * f + w;
+        const float w = s == -INFINITY ? 0.f : exp2f(s - m);
+        if (w == 0.f) continue;
+        any = true;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            o[e] = o[e] * f + (w == 0.f ? 0.f : w * __bfloat162float(vr[e]));
+            if (!isfinite(v[e])) o[e] += w * v[e];
     }
+    if (!any) return;
     __nv_bfloat16 *dst = p.out + (int64_t)q * p.out_stride + (int64_t)head * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16(o[e] / l);
+    for (int e = 0; e < E; ++e)
+        if (o[e] != 0.f) dst[e] = __float2bfloat16(__bfloat162float(dst[e]) + o[e]);
 }
 
 // Keys that a query of tile w sees (0: none, or no such tile).
@@ -299,10 +349,10 @@ __device__ void issuer(int n0, int n1, uint32_t sbase, uint32_t tmem, const Bars
 
 // Softmax and epilogue of tile w (4 warps, one row a thread: the TMEM lane
 // quarter that the warp may access).  Decisions before warp-wide TMEM accesses
-// are uniform.  `blocks`: of the CTA.
+// are uniform.
 template <int D>
 __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, const int (&n)[2],
-                        int blocks, int keys_cta, uint8_t *smem, uint32_t tmem,
+                        int keys_cta, uint8_t *smem, uint32_t tmem, int *odd_values,
                         const Bars<D> &bars, const WaitCtl &wc) {
     using L = Layout<D>;
     const int qd = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -314,9 +364,8 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
     const bool there = row < p.G * p.nt && i < tl.nq;
     const int see = p.causal ? min(tl.Lk, max(0, tl.see0 + i)) : tl.Lk;
     const int nkb = n[w];
-    // This tile reads the CTA's last value block first of the two (the issuer's
-    // order): it zeroes the rows behind the last key.
-    const bool clears = w == 0 ? n[0] == blocks : n[0] < blocks;
+    // The first block that some row of the CTA does not see whole.
+    const int part = (p.causal ? min(tl.Lk, max(0, tl.see0)) : tl.Lk) / kRows;
     float m = -INFINITY;  // of the raw scores
     float l = 0.f;
     for (int j = 0; j < nkb; ++j) {
@@ -382,14 +431,13 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
         float s0, s1;
         f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        // values behind the last key of the CTA become zeros (its last block alone)
-        if (clears && j == blocks - 1 && keys_cta - j * kRows < kRows) {
+        // a block seen in part: by the tile that reads its values first (the issuer's order)
+        if (j >= part && (w == 0 || j >= n[0])) {
             if (!mbar_wait_warp<false>(bars.full(fill_v(j)), bars.phase(fill_v(j)), wc)) return;
-            uint4 *v = reinterpret_cast<uint4 *>(smem + L::kRing +
-                                                 (fill_v(j) % L::kStages) * L::kTile);
-            for (int e = (keys_cta - j * kRows) * 8 + row; e < kRows * 8; e += 128)
-#pragma unroll
-                for (int a = 0; a < D / 64; ++a) v[a * (kAtom / 16) + e] = make_uint4(0, 0, 0, 0);
+            const bool behind = j * kRows + row >= keys_cta;
+            if ((p.causal || behind) &&
+                clean_row<D>(smem + L::kRing + (fill_v(j) % L::kStages) * L::kTile, row, behind))
+                *odd_values = 1;
             fence_proxy_async_smem();  // read by the tensor core (async proxy)
         }
         tmem_st_wait();
@@ -403,7 +451,6 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     __nv_bfloat16 *dst = p.out + (int64_t)(tl.q0 + i) * p.out_stride + (int64_t)head * D;
-    float probe = 0.f;  // NaN once an output is not finite
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t acc[32];
@@ -416,10 +463,7 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
         }
         float o[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            o[c] = see > 0 ? __uint_as_float(acc[c]) * inv : 0.f;
-            probe = fmaf(o[c], 0.f, probe);
-        }
+        for (int c = 0; c < 32; ++c) o[c] = see > 0 ? __uint_as_float(acc[c]) * inv : 0.f;
         if (there) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -429,14 +473,17 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
                                nact_pack(o[8 * c + 6], o[8 * c + 7]));
         }
     }
-    if (p.causal) {
-        unsigned bad = __ballot_sync(0xffffffffu, there && see > 0 && probe != probe);
-        while (bad) {
-            const int b = __ffs(bad) - 1;
-            bad &= bad - 1;
-            slow_row<D>(p, tl.q0 + __shfl_sync(0xffffffffu, i, b),
-                        __shfl_sync(0xffffffffu, head, b), kvh, tl.k0,
-                        __shfl_sync(0xffffffffu, see, b));
+    // (set before the last p_full that o_full came after)
+    if (*reinterpret_cast<volatile int *>(odd_values)) {
+        __syncwarp();
+        unsigned rows = __ballot_sync(0xffffffffu, there && see > part * kRows);
+        const float ms = m == -INFINITY ? 0.f : m * p.scale_log2;
+        while (rows) {
+            const int b = __ffs(rows) - 1;
+            rows &= rows - 1;
+            put_back<D>(p, tl.q0 + __shfl_sync(0xffffffffu, i, b),
+                        __shfl_sync(0xffffffffu, head, b), kvh, tl.k0, part * kRows,
+                        __shfl_sync(0xffffffffu, see, b), __shfl_sync(0xffffffffu, ms, b));
         }
     }
 }
@@ -455,6 +502,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
     const Bars<D> bars{sbase + L::kBars};
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kBars + 240);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kBars + 244);
+    int *odd_values = reinterpret_cast<int *>(smem + L::kBars + 248);
     if (threadIdx.x == 0) {
         mbar_init(bars.q_full(), 1);
         mbar_init(bars.drain(), 1);
@@ -468,6 +516,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
             mbar_init(bars.empty(s), 1);
         }
         *abort_flag = 0;
+        *odd_values = 0;
         fence_mbar_init();
         tma_prefetch_desc(&mQ);
         tma_prefetch_desc(&mK);
@@ -491,7 +540,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         if (tl.nq > 0)
-            softmax<D>(p, tl, warp >> 2, kvh, n, blocks, keys_cta, smem, tmem, bars, wc);
+            softmax<D>(p, tl, warp >> 2, kvh, n, keys_cta, smem, tmem, odd_values, bars, wc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8 && blocks > 0)
