@@ -254,7 +254,8 @@ wanvae_status wanvae_packed_attention(const void *q, int64_t q_stride, const voi
  *   k, v  : [n_pages][n_kv_heads][page_size][head_dim], of type dt
  *   dt    : WANVAE_BF16, or WANVAE_E4M3: a row (one token, one head) holds
  *           e4m3 elements q and one E8M0 scale, x[d] = q[d] * 2^(code - 127)
- *   k_exp, v_exp : [n_pages][n_kv_heads][page_size] scale codes (E4M3 only)
+ *   k_exp, v_exp : [n_pages][n_kv_heads][page_size] scale codes (E4M3 only), 27
+ *           to 247 (2^-100 to 2^120) in rows that attention reads
  *   page_size : 16, 32, 64, .. 1024.  head_dim : 64 or 128. */
 typedef struct {
     void *k, *v;
@@ -273,8 +274,10 @@ typedef struct {
  *   cu_new : device int32 [n_seq + 1]: sequence s's new tokens are rows
  *            cu_new[s] .. cu_new[s+1] - 1, its last positions; NULL: one new
  *            token for each sequence (total = n_seq)
- * A token whose position or page lies outside the page table or the cache is
- * not written, and wanvae_sync_status reports WANVAE_ERR_CUDA.
+ * No two tokens of a call may lie in the same slot (sequences may share pages that
+ * the call does not write).  A token whose position or page lies outside the page
+ * table or the cache is not written, and wanvae_sync_status reports
+ * WANVAE_ERR_CUDA.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_kv_cache_append(const wanvae_kv_cache *cache, const void *k,
                                      int64_t k_stride, const void *v, int64_t v_stride,
@@ -284,9 +287,10 @@ wanvae_status wanvae_kv_cache_append(const wanvae_kv_cache *cache, const void *k
 
 /* The cache read back, packed, for wanvae_packed_attention over new tokens:
  * positions 0 .. of sequence s to the rows cu[s] .. cu[s+1] - 1 of k and v
- * (bf16 [total][n_kv_heads][head_dim], tokens k_stride / v_stride apart).  Rows
- * behind the last sequence, and rows whose page lies outside the page table
- * or the cache (reported as for wanvae_kv_cache_append), are left as they were.
+ * (bf16 [total][n_kv_heads][head_dim], tokens k_stride / v_stride apart; both
+ * may lie side by side in rows of one buffer).  Rows behind the last sequence,
+ * and rows whose page lies outside the page table or the cache (reported as for
+ * wanvae_kv_cache_append), are left as they were.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t *page_table,
                                      int64_t max_pages, const int32_t *cu, int64_t n_seq,

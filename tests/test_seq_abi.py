@@ -115,6 +115,24 @@ def test_no_cache_is_refused(lib):
                                       None) == ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("edit", [
+    dict(v=Q + 240), dict(v=Q + 16), dict(v=Q + 256, ks=248, vs=248),
+    dict(v=Q + 256, ks=256, vs=264), dict(v=Q + 512 - 16, ks=256, vs=256),
+    dict(v=Q - 512 + 16, ks=256, vs=256)])
+def test_gather_refuses_rows_that_collide(lib, edit):
+    """10 rows of 2 heads of 64 elements (256 bytes) each."""
+    assert gather(lib, **edit) == ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("edit,want", [
+    # 64 sequences of 2^20 rows with 64 query heads: fits 32 bits; 2^29 rows and more do not
+    (dict(n=64, pages=2 ** 16, qs=64 * 64, os=64 * 64, hq=64, bytes=10 ** 8, ws=None), ERR_WORKSPACE),
+    (dict(n=1, pages=2 ** 25, ws=None), ERR_UNSUPPORTED),
+    (dict(n=65535, pages=2 ** 16, ws=None), ERR_UNSUPPORTED)])
+def test_paged_attention_counts_in_32_bits(lib, edit, want):
+    assert decode(lib, **edit) == want
+
+
 def test_append_without_offsets_is_one_row_a_sequence(lib):
     assert append(lib, cu=None) == ERR_INVALID_ARG
     assert append(lib, lens=None) == ERR_INVALID_ARG
@@ -161,7 +179,9 @@ def norm(lib, **edit):
     (dict(eps=math.nan), ERR_INVALID_ARG), (dict(scale=math.inf), ERR_INVALID_ARG),
     (dict(scale=math.nan), ERR_INVALID_ARG), (dict(gp=C + 4), ERR_MISALIGNED),
     (dict(y=V + 8), ERR_MISALIGNED), (dict(y=Q), ERR_INVALID_ARG), (dict(n=K), ERR_INVALID_ARG),
-    (dict(n=V + 128), ERR_INVALID_ARG)])
+    (dict(n=V + 128), ERR_INVALID_ARG), (dict(gp=V + 64), ERR_INVALID_ARG),
+    (dict(gp=V - 64), ERR_INVALID_ARG), (dict(gate=O - 99 * 256), ERR_INVALID_ARG),
+    (dict(gate=O - 256, per=2 ** 62, gn=O), ERR_INVALID_ARG)])
 def test_gated_norm_refuses(lib, edit, want):
     assert norm(lib, **edit) == want
 

@@ -27,6 +27,18 @@ size_t span(int64_t n, int64_t stride, int64_t width) {
     return n < 1 ? 0 : ((size_t)(n - 1) * stride + width) * 2;
 }
 
+// Whether rows of two tensors collide: n tokens of `width` elements each, which may
+// lie side by side in one buffer where their strides are equal.
+bool rows_collide(const void *a, int64_t a_stride, const void *b, int64_t b_stride, int64_t n,
+                  int64_t width) {
+    if (!overlap(a, span(n, a_stride, width), b, span(n, b_stride, width))) return false;
+    if (a_stride != b_stride) return true;
+    const int64_t s = a_stride * 2, w = width * 2;
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    const int64_t off = (d % s + s) % s;  // from a row of a to the next row of b
+    return off < w || off > s - w;
+}
+
 wanvae_status from_cuda(cudaError_t e) { return e == cudaSuccess ? WANVAE_OK : WANVAE_ERR_CUDA; }
 
 // Tokens and widths as the kernels count them (int32), strides within a tensor
@@ -179,9 +191,9 @@ wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t
     if (!stride_ok(k_stride, w) || !stride_ok(v_stride, w)) return WANVAE_ERR_INVALID_ARG;
     if (misaligned(k) || misaligned(v) || misaligned(cu, 4) || misaligned(page_table, 4))
         return WANVAE_ERR_MISALIGNED;
-    const size_t kb = span(total, k_stride, w), vb = span(total, v_stride, w);
-    // k and v may lie side by side in one buffer, their rows interleaved
-    if (k == v || touches(s, k, kb) || touches(s, v, vb)) return WANVAE_ERR_INVALID_ARG;
+    if (rows_collide(k, k_stride, v, v_stride, total, w) ||
+        touches(s, k, span(total, k_stride, w)) || touches(s, v, span(total, v_stride, w)))
+        return WANVAE_ERR_INVALID_ARG;
     LaunchCtx ctx;
     if (!make_launch_ctx(ctx, stream)) return WANVAE_ERR_CUDA;
     count_launches(1);
@@ -213,10 +225,11 @@ wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
     if (!(scale > 0.f) || !(scale < INFINITY)) return WANVAE_ERR_INVALID_ARG;
     const size_t need = wanvae_paged_attention_workspace_size(n_heads, s.H, s.D);
     if (need == 0) return WANVAE_ERR_UNSUPPORTED;
-    // units of 16 rows that the page table could hold, and one more an item, are
-    // counted in 32 bits
-    const int64_t units = ((max_pages << s.log2_page) + 15) / 16 + 1;
-    if (units > INT32_MAX / 64 || units * n_seq > INT32_MAX / n_heads) return WANVAE_ERR_UNSUPPORTED;
+    // rows of a sequence, and units of 64 rows that the page table could hold (one more
+    // an item, an item for each kv head and 8 query heads), are counted in 32 bits
+    const int64_t units = ((max_pages << s.log2_page) + 63) / 64 + 1;
+    const int64_t items = n_seq * s.H * ((n_heads / s.H + 7) / 8);
+    if (units > INT32_MAX / 256 || units * items > INT32_MAX) return WANVAE_ERR_UNSUPPORTED;
     const int64_t w = n_heads * s.D;
     if (!stride_ok(q_stride, w) || !stride_ok(out_stride, w)) return WANVAE_ERR_INVALID_ARG;
     if (misaligned(q) || misaligned(out) || misaligned(lens, 4) || misaligned(page_table, 4))
@@ -250,6 +263,12 @@ wanvae_status wanvae_gated_residual_norm(const void *x, const void *f, const flo
         misaligned(gamma_pre) || misaligned(y) || misaligned(n))
         return WANVAE_ERR_MISALIGNED;
     const size_t bytes = (size_t)n_tokens * C * (dt == WANVAE_F32 ? 4 : 2);
+    const size_t row = (size_t)C * 4;
+    const size_t gates = gate ? (size_t)((n_tokens - 1) / tokens_per_gate + 1) * row : 0;
+    for (const void *o : {static_cast<const void *>(y), static_cast<const void *>(n)})
+        if (o && (overlap(gamma_post, gamma_post ? row : 0, o, bytes) ||
+                  overlap(gate, gates, o, bytes) || overlap(gamma_pre, gamma_pre ? row : 0, o, bytes)))
+            return WANVAE_ERR_INVALID_ARG;
     if (overlap(x, bytes, y, bytes) || overlap(f, bytes, y, bytes) ||
         (n && (overlap(x, bytes, n, bytes) || overlap(f, bytes, n, bytes) ||
                overlap(y, bytes, n, bytes))))
