@@ -9,22 +9,34 @@
 // A CTA owns one kv head and two tiles of 128 rows of one sequence, each 128 / G
 // consecutive queries times the G query heads of the group, so that short
 // prompts fill the tensor core's rows, keys are read once for the group, and
-// a causal tile's diagonal is G times shorter.  It sweeps the visible keys in
-// blocks of 128, and for each tile
-//   S = Q K_j^T       (tcgen05, S in TMEM)
-//   P = exp2(S' - m)  (a warpgroup of its own, one row a thread; P over S in TMEM)
-//   O += P V_j        (tcgen05, P from TMEM, V as it lies in memory, read along its rows)
-// While one tile's warpgroup computes exponentials the tensor core runs the
-// other tile's products: O += P V_j and the next S of a tile are issued together
-// as soon as its P is there (MMAs of one thread run in order, so the next S may
-// overwrite the P that the product before it reads).  The running maximum m
-// moves only by more than 2^8, as in the mid-block's core, so P stays <= 256 and
-// O is rarely rescaled, by the tile's own warpgroup.  P rounds to bf16, the type
-// that V has (an MMA's operands share one); the sum is of the unrounded P.
+// a causal tile's diagonal is G times shorter.  It sweeps the visible keys, and for
+// each tile, turn by turn,
+//   S = Q K_u^T       (tcgen05, S in TMEM)
+//   P = exp2(S' - m)  (a warpgroup of its own, one row a thread; P in TMEM)
+//   O += P V_u        (tcgen05, P from TMEM, V as it lies in memory, read along its rows)
+// Each tile has an issuing warp of its own (one warp for both, which waits for one
+// tile while the other's P is there: 324 and 1319 us for the two examples below) and
+// its next S is under way while the warpgroup computes exponentials:
+//   D = 128: O of both tiles takes half of TMEM, S and P the rest.  A turn is 64
+//     keys, with two places for S a tile; P lies over its S, and the place's next S is
+//     issued behind the product that reads P (MMAs of one thread run in order).  Turns of 128
+//     keys with one place, where S waits for P's product: 318 us.
+//   D = 64: a turn is 128 keys with one place for S and columns of its own for P
+//     (kApart); the next S is issued as soon as the warpgroup has read the last one.
+//     Turns of 64 keys as above: 1440 us, their waits and Q's reads counting twice.
+// The running maximum m moves only by more than 2^8, as in the mid-block's core, so P
+// stays <= 256 and O is rarely rescaled, by the tile's own warpgroup.  P rounds to
+// bf16, the type that V has (an MMA's operands share one); the sum is of the
+// unrounded P.  (Taking the first half's weights from the maximum so far while the
+// turn's is found changed nothing: 333 us.)
 //
-// What bounds it: for D = 128 a block of both tiles is 1024 cycles of MMAs and,
-// per SM quarter, 256 warp instructions of exponentials among about 800; for
-// D = 64 the MMAs halve and the exponentials do not.
+// What bounds it: for D = 128 the tensor core, 2048 cycles of MMAs for 128 keys of both
+// tiles (Q K^T reads both operands from shared memory, 48 cycles an MMA of 64 columns, not
+// 16) of about 2900; 16 query and 4 kv heads over causal prompts of 8192, 5003, 188 and
+// 3001 tokens: 304 us, 1.36 PFLOP/s, 0.70 of the measured matrix rate.  For D = 64 the
+// threads: 128 keys of both tiles are 1460 cycles of exponentials, sums, maxima and
+// roundings on an SM quarter (1024 of them MUFU's) of about 2300; 21 frames of 6240
+// tokens, 6 heads, full: 1190 us, 1.05 PFLOP/s, 0.54.
 //
 // Masked scores are replaced, never added to, so nothing in a masked key
 // reaches a row.  A masked value's weight is zero, but 0 * NaN is not: of the blocks
@@ -46,7 +58,7 @@
 namespace wanvae {
 namespace {
 
-constexpr int kThreads = 384;  // two softmax warpgroups; issuer, producer, two idle warps
+constexpr int kThreads = 384;  // two softmax warpgroups; two issuers, producer, an idle warp
 // Registers: 384 threads launch with 168 (64512 in all); the third warpgroup
 // gives back what the softmax warpgroups take: 2 * 128 * 216 + 128 * 72 = 64512.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
@@ -81,8 +93,22 @@ struct Layout {
     static constexpr int kStages = D == 64 ? 8 : 5;      // blocks of K and V in flight
     static constexpr uint32_t kQ = 0, kRing = 2 * kTile;
     static constexpr uint32_t kBars = kRing + kStages * kTile;
-    static constexpr uint32_t kSmem = 1024 + kBars + 256;
-    static constexpr uint32_t kO = 256;  // TMEM: S and P of tile w at 128 w, O at 256 + 128 w
+    static constexpr uint32_t kSmem = 1024 + kBars + 272;
+    // Keys of a turn, turns of a block.  TMEM columns of tile w: S of turn u, its P over S or
+    // (kApart) in columns of its own, O.
+    static constexpr bool kApart = D == 64;
+    static constexpr int kTurn = kApart ? 128 : 64, kPer = kRows / kTurn;
+    static __device__ __forceinline__ int block_of(int u) { return kApart ? u : u >> 1; }
+    static __device__ __forceinline__ int place_of(int u) { return kApart ? 0 : u & 1; }
+    static __device__ __forceinline__ uint32_t s_col(int w, int u) {
+        return 128u * w + (kApart ? 0u : 64u * (u & 1));
+    }
+    static __device__ __forceinline__ uint32_t p_col(int w, int u) {
+        return kApart ? 256u + 64u * w : s_col(w, u);
+    }
+    static __device__ __forceinline__ uint32_t o_col(int w) {
+        return kApart ? 384u + 64u * w : 256u + 128u * w;
+    }
 };
 
 // The ring holds K_0, V_0, K_1, V_1, ..
@@ -94,15 +120,23 @@ struct Bars {
     static constexpr int kStages = Layout<D>::kStages;
     uint32_t base;
     __device__ uint32_t q_full() const { return base; }
-    __device__ uint32_t drain() const { return base + 8; }
-    __device__ uint32_t s_full(int w) const { return base + 16 + 8 * w; }
-    __device__ uint32_t p_full(int w) const { return base + 32 + 8 * w; }
-    __device__ uint32_t o_full(int w) const { return base + 48 + 8 * w; }
-    __device__ uint32_t full(int fill) const { return base + 64 + 8 * (fill % kStages); }
+    __device__ uint32_t drain(int w) const { return base + 8 + 8 * w; }
+    __device__ uint32_t o_done(int w) const { return base + 24 + 8 * w; }
+    // of a turn's S and P (phase_of_turn): two turns' worth, or one and S read (kApart)
+    static constexpr bool kApart = Layout<D>::kApart;
+    static __device__ int buf(int u) { return kApart ? 0 : u & 1; }
+    __device__ uint32_t s_full(int w, int u) const { return base + 40 + 16 * w + 8 * buf(u); }
+    __device__ uint32_t p_full(int w, int u) const { return base + 72 + 16 * w + 8 * buf(u); }
+    __device__ uint32_t s_free(int w) const { return base + 48 + 16 * w; }
+    __device__ uint32_t o_full(int w) const { return base + 104 + 8 * w; }
+    __device__ uint32_t full(int fill) const { return base + 120 + 8 * (fill % kStages); }
     __device__ uint32_t empty(int fill) const {
-        return base + 64 + 8 * (kStages + fill % kStages);
+        return base + 120 + 8 * (kStages + fill % kStages);
     }
     static __device__ uint32_t phase(int fill) { return (uint32_t)(fill / kStages) & 1u; }
+    static __device__ uint32_t phase_of_turn(int u) {
+        return (uint32_t)(kApart ? u : u >> 1) & 1u;
+    }
 };
 
 // Tile pair `x` of the launch, counting the pairs of every sequence in order;
@@ -160,10 +194,10 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 
 // A value row of a block in shared memory (row `row` of 128, the blocks of 64
 // elements kAtom apart): zeros where `behind`, else without its elements that are
-// not finite; true where it had any.  The row's 16-byte pieces are taken in any
+// not finite, and *odd set where it had any.  The row's 16-byte pieces are taken in any
 // order (the swizzle stays within a row), a different one by each of eight lanes.
 template <int D>
-__device__ __forceinline__ bool clean_row(uint8_t *block, int row, bool behind) {
+__device__ __forceinline__ void clean_row(uint8_t *block, int row, bool behind, int *odd) {
     uint32_t m = 0;
     uint4 *v = reinterpret_cast<uint4 *>(block) + row * 8;
 #pragma unroll
@@ -179,7 +213,9 @@ __device__ __forceinline__ bool clean_row(uint8_t *block, int row, bool behind) 
             m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
                                      __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
         }
-    if (!not_finite(m)) return false;
+    if (!not_finite(m)) return;
+    *odd = 1;
+    __threadfence_block();  // who finds the zeros finds this too
     for (int a = 0; a < D / 64; ++a)
         for (int c = 0; c < 8; ++c) {
             uint4 x = v[a * (kAtom / 16) + c];
@@ -189,7 +225,6 @@ __device__ __forceinline__ bool clean_row(uint8_t *block, int row, bool behind) 
             x.w &= ~not_finite(x.w);
             v[a * (kAtom / 16) + c] = x;
         }
-    return true;
 }
 
 // Adds to a row that is written the value elements that clean_row took out of the keys
@@ -241,7 +276,10 @@ __device__ __forceinline__ int keys_of(const PackedArgs &p, const Tile &tl, int 
     if (nq <= 0) return 0;
     return p.causal ? min(tl.Lk, max(0, tl.see0 + w * p.nt + nq - 1)) : tl.Lk;
 }
-__device__ __forceinline__ int blocks_of(int keys) { return (keys + kRows - 1) / kRows; }
+template <int D>
+__device__ __forceinline__ int turns_of(int keys) {
+    return (keys + Layout<D>::kTurn - 1) / Layout<D>::kTurn;
+}
 
 // TMA producer (one thread): Q, then K_0, V_0, K_1, ..
 template <int D>
@@ -274,75 +312,87 @@ __device__ void producer(const CUtensorMap *mQ, const CUtensorMap *mK, const CUt
     }
 }
 
-// MMA issuer (one warp).  Tile w takes part in blocks j < n[w].
+// MMA issuer of tile w (one warp), which has n turns in the first of the CTA's blocks.
 template <int D>
-__device__ void issuer(int n0, int n1, uint32_t sbase, uint32_t tmem, const Bars<D> &bars,
-                       const WaitCtl &wc) {
+__device__ void issuer(int w, int n, int blocks, uint32_t sbase, uint32_t tmem,
+                       const Bars<D> &bars, const WaitCtl &wc) {
     using L = Layout<D>;
-    const uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32_bt(128, D);
-    const uint64_t q0 = sdesc_kmajor(sbase + L::kQ, 128u, kLayoutSw128);
+    constexpr int kTurn = L::kTurn, kPer = L::kPer, kAhead = L::kApart ? 1 : 2;
+    const uint32_t id_s = idesc_bf16_f32(128, kTurn), id_o = idesc_bf16_f32_bt(128, D);
+    const uint64_t q0 = sdesc_kmajor(sbase + L::kQ + w * L::kTile, 128u, kLayoutSw128);
     const uint64_t k0 = sdesc_kmajor(sbase + L::kRing, 128u, kLayoutSw128);
     const uint64_t v0 = sdesc_rows_sw128(sbase + L::kRing, kAtom);
-    constexpr uint32_t kTile16 = L::kTile >> 4;
-    const int blocks = max(n0, n1);
-    auto scores = [&](int w, int j) {  // S = Q K_j^T (in the elected lane)
-        const uint64_t a = q0 + (uint32_t)w * kTile16;
-        const uint64_t b = k0 + (uint32_t)(fill_k(j) % L::kStages) * kTile16;
+    const uint32_t to = tmem + L::o_col(w);
+    auto part_of = [](int f, int u) {  // a turn's rows of a block in the ring
+        return (uint32_t)(f % L::kStages) * (L::kTile >> 4) +
+               (uint32_t)L::place_of(u) * (kTurn * 128 >> 4);
+    };
+    auto ends_block = [&](int u) { return L::place_of(u) == kPer - 1 || u + 1 == n; };
+    auto scores = [&](int u) {  // S = Q K^T of a turn (in the elected lane)
+        const int f = fill_k(L::block_of(u));
+        const uint64_t b = k0 + part_of(f, u);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (uint32_t)(kk >> 2) * (kAtom >> 4) + (kk & 3) * 2;
-            mma_bf16_ss(tmem + 128u * w, a + off, b + off, id_s, kk > 0);
+            mma_bf16_ss(tmem + L::s_col(w, u), q0 + off, b + off, id_s, kk > 0);
         }
-        mma_commit(bars.s_full(w));
+        mma_commit(bars.s_full(w, u));
+        if (ends_block(u)) mma_commit(bars.empty(f));
     };
-    bool ok = mbar_wait_warp<false>(bars.q_full(), 0u, wc) &&
-              mbar_wait_warp<false>(bars.full(fill_k(0)), 0u, wc);
-    if (ok) {
+    bool ok = n == 0 || (mbar_wait_warp<false>(bars.q_full(), 0u, wc) &&
+                         mbar_wait_warp<false>(bars.full(fill_k(0)), 0u, wc));
+    if (ok && n > 0) {
         tc_fence_after();
         if (elect_one()) {
-            if (n0 > 0) scores(0, 0);
-            if (n1 > 0) scores(1, 0);
-            mma_commit(bars.empty(fill_k(0)));
+            scores(0);
+            if (kAhead > 1 && n > 1) scores(1);
         }
         __syncwarp();
     }
-    for (int j = 0; ok && j < blocks; ++j) {
-        ok = mbar_wait_warp<false>(bars.full(fill_v(j)), bars.phase(fill_v(j)), wc);
-        if (ok && j + 1 < blocks)
-            ok = mbar_wait_warp<false>(bars.full(fill_k(j + 1)), bars.phase(fill_k(j + 1)), wc);
-        const uint64_t b = v0 + (uint32_t)(fill_v(j) % L::kStages) * kTile16;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const int n = w ? n1 : n0;
-            if (!ok || j >= n) continue;
-            ok = mbar_wait_warp<false>(bars.p_full(w), (uint32_t)j & 1u, wc);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < kRows / 16; ++kk)
-                    mma_bf16_ts(tmem + L::kO + 128u * w, tmem + 128u * w + kk * 8,
-                                b + kk * (2048u >> 4), id_o, j > 0 || kk > 0);
-                if (j + 1 < n)
-                    scores(w, j + 1);
-                else
-                    mma_commit(bars.o_full(w));
+    for (int u = 0; ok && u < n; ++u) {
+        const int f = fill_v(L::block_of(u));  // (the next block's keys are fill f + 1)
+        const bool more = u + kAhead < n;
+        if (L::place_of(u) == 0) {
+            if (!L::kApart)
+                ok = mbar_wait_warp<false>(bars.full(f), bars.phase(f), wc);
+            if (more) ok = ok && mbar_wait_warp<false>(bars.full(f + 1), bars.phase(f + 1), wc);
+            if (L::kApart && more) {
+                ok = ok && mbar_wait_warp<false>(bars.s_free(w), bars.phase_of_turn(u), wc);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) scores(u + 1);
+                __syncwarp();
             }
-            __syncwarp();
+            if (L::kApart)
+                ok = ok && mbar_wait_warp<false>(bars.full(f), bars.phase(f), wc);
         }
+        ok = ok && mbar_wait_warp<false>(bars.p_full(w, u), bars.phase_of_turn(u), wc);
         if (!ok) break;
+        tc_fence_after();
         if (elect_one()) {
-            mma_commit(bars.empty(fill_v(j)));
-            if (j + 1 < blocks) mma_commit(bars.empty(fill_k(j + 1)));
+            const uint64_t b = v0 + part_of(f, u);
+#pragma unroll
+            for (int kk = 0; kk < kTurn / 16; ++kk)
+                mma_bf16_ts(to, tmem + L::p_col(w, u) + kk * 8, b + kk * (2048u >> 4), id_o,
+                            u > 0 || kk > 0);
+            mma_commit(u + 1 < n ? bars.o_done(w) : bars.o_full(w));
+            if (ends_block(u)) mma_commit(bars.empty(f));
+            if (!L::kApart && more) scores(u + 2);
         }
+        __syncwarp();
+    }
+    // the other tile's blocks (a place is given back once a turn: not before it is full)
+    for (int f = 2 * ((n + kPer - 1) / kPer); ok && f < 2 * blocks; ++f) {
+        ok = mbar_wait_warp<false>(bars.full(f), bars.phase(f), wc);
+        if (ok && elect_one()) mbar_arrive(bars.empty(f));
         __syncwarp();
     }
     // Every MMA issued above completes before TMEM is released.
     volatile int no_abort = 0;
     const WaitCtl dc{kDrainNs, wc.err, &no_abort, kDevErrTimeout | kDevErrDrain};
     if (elect_one()) {
-        mma_commit(bars.drain());
-        mbar_wait<false>(bars.drain(), 0u, dc);
+        mma_commit(bars.drain(w));
+        mbar_wait<false>(bars.drain(w), 0u, dc);
     }
     __syncwarp();
 }
@@ -351,35 +401,41 @@ __device__ void issuer(int n0, int n1, uint32_t sbase, uint32_t tmem, const Bars
 // quarter that the warp may access).  Decisions before warp-wide TMEM accesses
 // are uniform.
 template <int D>
-__device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, const int (&n)[2],
-                        int keys_cta, uint8_t *smem, uint32_t tmem, int *odd_values,
+__device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, int n, int keys_cta,
+                        uint8_t *smem, uint32_t tmem, int *odd_values,
                         const Bars<D> &bars, const WaitCtl &wc) {
     using L = Layout<D>;
+    constexpr int kTurn = L::kTurn;
     const int qd = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int row = qd * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(qd * 32) << 16);
-    const uint32_t ts = trow + 128u * w, to = trow + L::kO + 128u * w;
+    const uint32_t to = trow + L::o_col(w);
     const int r = row / p.G, head = kvh * p.G + row % p.G;
     const int i = w * p.nt + r;  // query of the CTA
     const bool there = row < p.G * p.nt && i < tl.nq;
     const int see = p.causal ? min(tl.Lk, max(0, tl.see0 + i)) : tl.Lk;
-    const int nkb = n[w];
     // The first block that some row of the CTA does not see whole.
     const int part = (p.causal ? min(tl.Lk, max(0, tl.see0)) : tl.Lk) / kRows;
     float m = -INFINITY;  // of the raw scores
     float l = 0.f;
-    for (int j = 0; j < nkb; ++j) {
-        if (!mbar_wait_warp<false>(bars.s_full(w), (uint32_t)j & 1u, wc)) return;
+    for (int u = 0; u < n; ++u) {
+        if (!mbar_wait_warp<false>(bars.s_full(w, u), bars.phase_of_turn(u), wc)) return;
         tc_fence_after();
-        uint32_t s[kRows];
+        const uint32_t ts = trow + L::s_col(w, u), tp = trow + L::p_col(w, u);
+        uint32_t s[kTurn];
 #pragma unroll
-        for (int c0 = 0; c0 < kRows; c0 += 32) tmem_ld32_async(ts + (uint32_t)c0, s + c0);
+        for (int c0 = 0; c0 < kTurn; c0 += 32) tmem_ld32_async(ts + (uint32_t)c0, s + c0);
 #pragma unroll
-        for (int c0 = 0; c0 < kRows; c0 += 32) tmem_ld_wait32(s + c0);
-        const int kvalid = see - j * kRows;
-        if (__any_sync(0xffffffffu, kvalid < kRows)) {
+        for (int c0 = 0; c0 < kTurn; c0 += 32) tmem_ld_wait32(s + c0);
+        if (L::kApart) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.s_free(w));
+        }
+        const int kvalid = see - u * kTurn;
+        if (__any_sync(0xffffffffu, kvalid < kTurn)) {
 #pragma unroll
-            for (int c = 0; c < kRows; ++c)
+            for (int c = 0; c < kTurn; ++c)
                 if (c >= kvalid) s[c] = 0xff800000u;  // -inf
         }
         float mx[4];
@@ -387,19 +443,22 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
         for (int c = 0; c < 4; ++c)
             mx[c] = fmaxf(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
 #pragma unroll
-        for (int c = 8; c < kRows; c += 8)
+        for (int c = 8; c < kTurn; c += 8)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         float f = 1.f;
-        if ((top - m) * p.scale_log2 > 8.f) {  // (also the first block's, from -inf)
+        if ((top - m) * p.scale_log2 > 8.f) {  // (also the first turn's, from -inf)
             if (m != -INFINITY) f = exp2_fast((m - top) * p.scale_log2);
             m = top;
         }
-        // O is whole up to the last block: S came after its product
-        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+        if (u > 0 && __any_sync(0xffffffffu, f != 1.f)) {
             l *= f;
+            // once the last turn's product is in O (the one before it was there before S,
+            // or, kApart, before the last P)
+            if (!mbar_wait_warp<false>(bars.o_done(w), (uint32_t)(u - 1) & 1u, wc)) return;
+            tc_fence_after();
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld32_async(to + (uint32_t)c0, o);
@@ -413,7 +472,7 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
         const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), ms2 = f32x2(-ms, -ms);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 64 keys, 32 columns of P at a time
+        for (int h = 0; h < kTurn / 64; ++h) {  // 64 keys, 32 columns of P at a time
             uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
@@ -426,26 +485,31 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
                 sum[c & 1] = add_f32x2(sum[c & 1], f32x2(a, b));
                 pk[c] = nact_pack(a, b);
             }
-            tmem_st32_async(ts + 32u * h, pk);
+            if (L::kApart && h == 0 && u > 0) {  // the last turn's product has read P
+                if (!mbar_wait_warp<false>(bars.o_done(w), (uint32_t)(u - 1) & 1u, wc)) return;
+                tc_fence_after();
+            }
+            tmem_st32_async(tp + 32u * h, pk);
         }
         float s0, s1;
         f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        // a block seen in part: by the tile that reads its values first (the issuer's order)
-        if (j >= part && (w == 0 || j >= n[0])) {
-            if (!mbar_wait_warp<false>(bars.full(fill_v(j)), bars.phase(fill_v(j)), wc)) return;
-            const bool behind = j * kRows + row >= keys_cta;
-            if ((p.causal || behind) &&
-                clean_row<D>(smem + L::kRing + (fill_v(j) % L::kStages) * L::kTile, row, behind))
-                *odd_values = 1;
+        // a block seen in part (both tiles' warpgroups clean it: the same zeros)
+        if (L::place_of(u) == 0 && L::block_of(u) >= part) {
+            const int fv = fill_v(L::block_of(u));
+            if (!mbar_wait_warp<false>(bars.full(fv), bars.phase(fv), wc)) return;
+            const bool behind = u * kTurn + row >= keys_cta;
+            if (p.causal || behind)
+                clean_row<D>(smem + L::kRing + (fv % L::kStages) * L::kTile, row, behind,
+                             odd_values);
             fence_proxy_async_smem();  // read by the tensor core (async proxy)
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.p_full(w));
+        if (lane == 0) mbar_arrive(bars.p_full(w, u));
     }
-    if (nkb > 0) {
+    if (n > 0) {
         if (!mbar_wait_warp<false>(bars.o_full(w), 0u, wc)) return;
         tc_fence_after();
     }
@@ -454,7 +518,7 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t acc[32];
-        if (nkb > 0) {
+        if (n > 0) {
             tmem_ld32_async(to + (uint32_t)c0, acc);
             tmem_ld_wait32(acc);
         } else {
@@ -491,7 +555,7 @@ __device__ void softmax(const PackedArgs &p, const Tile &tl, int w, int kvh, con
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-                   const __grid_constant__ CUtensorMap mV, const PackedArgs p) {
+                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ PackedArgs p) {
     using L = Layout<D>;
     griddep_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
@@ -500,20 +564,24 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
     const uint32_t sbase = smem_u32(smem);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const Bars<D> bars{sbase + L::kBars};
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kBars + 240);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kBars + 244);
-    int *odd_values = reinterpret_cast<int *>(smem + L::kBars + 248);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kBars + 256);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kBars + 260);
+    int *odd_values = reinterpret_cast<int *>(smem + L::kBars + 264);
     if (threadIdx.x == 0) {
         mbar_init(bars.q_full(), 1);
-        mbar_init(bars.drain(), 1);
         for (int w = 0; w < 2; ++w) {
-            mbar_init(bars.s_full(w), 1);
-            mbar_init(bars.p_full(w), 4);
+            mbar_init(bars.drain(w), 1);
+            mbar_init(bars.o_done(w), 1);
             mbar_init(bars.o_full(w), 1);
+            for (int u = 0; u < L::kPer; ++u) {
+                mbar_init(bars.s_full(w, u), 1);
+                mbar_init(bars.p_full(w, u), 4);
+            }
+            if (L::kApart) mbar_init(bars.s_free(w), 4);
         }
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bars.full(s), 1);
-            mbar_init(bars.empty(s), 1);
+            mbar_init(bars.empty(s), 2);
         }
         *abort_flag = 0;
         *odd_values = 0;
@@ -535,18 +603,20 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
     const int kvh = blockIdx.x % p.Hkv;
     const Tile tl = find_tile(p, blockIdx.x / p.Hkv);
     const int keys[2] = {keys_of(p, tl, 0), keys_of(p, tl, 1)};
-    const int n[2] = {blocks_of(keys[0]), blocks_of(keys[1])};
-    const int keys_cta = max(keys[0], keys[1]), blocks = max(n[0], n[1]);
+    const int n0 = turns_of<D>(keys[0]), n1 = turns_of<D>(keys[1]);
+    const int keys_cta = max(keys[0], keys[1]), blocks = (max(n0, n1) + L::kPer - 1) / L::kPer;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         if (tl.nq > 0)
-            softmax<D>(p, tl, warp >> 2, kvh, n, keys_cta, smem, tmem, odd_values, bars, wc);
+            softmax<D>(p, tl, warp >> 2, kvh, warp >> 2 ? n1 : n0, keys_cta, smem, tmem, odd_values, bars, wc);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8 && blocks > 0)
-            issuer<D>(__shfl_sync(0xffffffffu, n[0], 0), __shfl_sync(0xffffffffu, n[1], 0), sbase,
+        const int w = warp - 8;
+        if (w < 2 && blocks > 0)
+            issuer<D>(w, __shfl_sync(0xffffffffu, w ? n1 : n0, 0),
+                      __shfl_sync(0xffffffffu, blocks, 0), sbase,
                       __shfl_sync(0xffffffffu, tmem, 0), bars, wc);
-        if (warp == 9 && lane == 0 && blocks > 0)
+        if (w == 2 && lane == 0 && blocks > 0)
             producer<D>(&mQ, &mK, &mV, p, tl, kvh, blocks, sbase, bars, wc);
     }
     __syncwarp();
