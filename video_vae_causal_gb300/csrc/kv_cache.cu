@@ -15,7 +15,10 @@
 // Rows lie [page][head][slot][D]: the rows of one head and page are
 // contiguous, which is how attention over the cache reads them.  Both passes
 // move each row once (2 D bytes on one side, D + 1 on the other) and are bound
-// by HBM.  A row takes D / 8 lanes with one 16-byte vector of bf16 each; a
+// by HBM: 75000 tokens of 8 heads of 128 read back take 78 us (5.8 TB/s, 0.86 of
+// the measured copy rate), 16384 tokens written 27 us (3.7 TB/s, 0.55: a warp has
+// five tokens, whose places, loads and rows' maxima it waits for in turn; loading the next
+// pass's rows as each is used spilled and took 29 us).  A row takes D / 8 lanes with one 16-byte vector of bf16 each; a
 // warp keeps the rows of a token's heads together and takes tokens in a row, so
 // that a token's page is looked up once for all heads and its sequence once for the
 // tokens that follow it.
@@ -32,8 +35,12 @@ namespace wanvae {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFlight = 8;  // rows of a lane's that are loaded before the first is used
-constexpr int kBlocks = 3;  // resident blocks that leave the registers for them
+// Rows of a lane's that are loaded before the first is used, and resident blocks that
+// leave the registers for them.  Sixteen prompts of 75000 tokens and 8 heads of 128
+// read back, in us: 8 rows and 3 blocks 81.7, 4 and 4 79.6, 4 and 5 77.7, 4 and 6 87
+// (spills), 2 and 6 82.3, 2 and 8 81.6.
+constexpr int kFlight = 4;
+constexpr int kBlocks = 5;
 constexpr int kExpMin = -100, kExpMax = 120;
 
 struct CacheArgs {
@@ -114,21 +121,27 @@ __device__ __forceinline__ uint4 dequantise8(const uint2 &q, uint32_t code) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The first token of this warp (ahead 0) or of the next one: `total` tokens over
+// `warps` warps, in order, to within one of each other.
+__device__ __forceinline__ int first_token(int total, int warps, int ahead) {
+    const int64_t id = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) + ahead;
+    return (int)(min(id, (int64_t)warps) * total / warps);
+}
+
 // Rows cu_new[s] .. of k and v to the last positions of sequence s.
 template <int D, bool kQuant>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 kv_append_kernel(const CacheArgs c, const __nv_bfloat16 *__restrict__ k, int64_t k_stride,
                  const __nv_bfloat16 *__restrict__ v, int64_t v_stride,
                  const int32_t *__restrict__ lens, const int32_t *__restrict__ cu_new, int n_seq,
-                 int total, int per_warp) {
+                 int total, int warps) {
     griddep_launch_dependents();
     griddep_wait();
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a warp holds
     const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
-    const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int t1 = (int)min((int64_t)total, (id + 1) * per_warp);
+    const int t1 = first_token(total, warps, 1);
     int seq = 0, first = 0, end = 0, len = 0;
-    for (int t = (int)min(id * per_warp, (int64_t)total); t < t1; ++t) {
+    for (int t = first_token(total, warps, 0); t < t1; ++t) {
         // the token's H key rows, then its H value rows, kFlight turns' loads at a time; the
         // first are in flight while the token's place is looked up
         const int64_t kt = t * k_stride, vt = t * v_stride;
@@ -189,16 +202,15 @@ kv_append_kernel(const CacheArgs c, const __nv_bfloat16 *__restrict__ k, int64_t
 template <int D, bool kQuant>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 kv_gather_kernel(const CacheArgs c, const int32_t *__restrict__ cu, int n_seq, int total,
-                 int per_warp, __nv_bfloat16 *__restrict__ k, int64_t k_stride, __nv_bfloat16 *__restrict__ v,
+                 int warps, __nv_bfloat16 *__restrict__ k, int64_t k_stride, __nv_bfloat16 *__restrict__ v,
                  int64_t v_stride) {
     griddep_launch_dependents();
     griddep_wait();
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int lane = threadIdx.x & 31, sub = lane % kLanes, grp = lane / kLanes;
-    const int64_t id = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int t1 = (int)min((int64_t)total, (id + 1) * per_warp);
+    const int t1 = first_token(total, warps, 1);
     int seq = 0, first = 0, end = 0;
-    for (int t = (int)min(id * per_warp, (int64_t)total); t < t1; ++t) {
+    for (int t = first_token(total, warps, 0); t < t1; ++t) {
         if (t >= end) {
             seq = seq_of_row(cu, n_seq, t);
             first = __ldg(cu + seq);
@@ -258,15 +270,11 @@ CacheArgs cache_args(const KvCacheSpec &c, const int32_t *table, int max_pages,
     return a;
 }
 
-// Tokens of a warp: one resident wave's share.
-int tokens_per_warp(int total, const LaunchCtx &ctx) {
-    const int warps = ctx.num_sms * kBlocks * (kThreads / 32);
-    return total / warps + (total % warps ? 1 : 0);
+// Warps of a launch: one resident wave, or one for each token.
+int warps_for(int total, const LaunchCtx &ctx) {
+    return std::min(total, ctx.num_sms * kBlocks * (kThreads / 32));
 }
-unsigned blocks_for(int total, int per_warp) {
-    const int warps = (total + per_warp - 1) / per_warp;
-    return (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
-}
+unsigned blocks_for(int warps) { return (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)); }
 
 }  // namespace
 
@@ -277,11 +285,11 @@ cudaError_t launch_kv_append(const KvCacheSpec &c, const void *k, int64_t k_stri
     const CacheArgs a = cache_args(c, table, max_pages, ctx);
     auto *kp = static_cast<const __nv_bfloat16 *>(k);
     auto *vp = static_cast<const __nv_bfloat16 *>(v);
-    const int per_warp = tokens_per_warp(total, ctx);
-    const dim3 grid(blocks_for(total, per_warp)), block(kThreads);
+    const int warps = warps_for(total, ctx);
+    const dim3 grid(blocks_for(warps)), block(kThreads);
     auto go = [&](auto kern) {
         return launch_pdl(kern, grid, block, 0, ctx, a, kp, k_stride, vp, v_stride, lens, cu_new,
-                          n_seq, total, per_warp);
+                          n_seq, total, warps);
     };
     if (c.D == 64) return c.e4m3 ? go(kv_append_kernel<64, true>) : go(kv_append_kernel<64, false>);
     if (c.D == 128)
@@ -295,10 +303,10 @@ cudaError_t launch_kv_gather(const KvCacheSpec &c, const int32_t *table, int max
     const CacheArgs a = cache_args(c, table, max_pages, ctx);
     auto *kp = static_cast<__nv_bfloat16 *>(k);
     auto *vp = static_cast<__nv_bfloat16 *>(v);
-    const int per_warp = tokens_per_warp(total, ctx);
-    const dim3 grid(blocks_for(total, per_warp)), block(kThreads);
+    const int warps = warps_for(total, ctx);
+    const dim3 grid(blocks_for(warps)), block(kThreads);
     auto go = [&](auto kern) {
-        return launch_pdl(kern, grid, block, 0, ctx, a, cu, n_seq, total, per_warp, kp, k_stride,
+        return launch_pdl(kern, grid, block, 0, ctx, a, cu, n_seq, total, warps, kp, k_stride,
                           vp, v_stride);
     };
     if (c.D == 64) return c.e4m3 ? go(kv_gather_kernel<64, true>) : go(kv_gather_kernel<64, false>);
