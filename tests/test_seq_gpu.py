@@ -458,20 +458,31 @@ def test_cache_bad_pages_are_left_out(cuda_lib):
 
 
 # ------------------------------------------------------------------ one token over the cache
+# What a call runs depends on how far its page table reaches: 8-bit caches of 128-element
+# heads behind long tables have a kernel of their own.
+def widened(table, page, hkv):
+    """The table, reaching 2^18 rows over all sequences and kv heads and 4096 in each."""
+    reach = max(4096, -(-2 ** 18 // (table.shape[0] * hkv)))
+    out = torch.full((table.shape[0], -(-reach // page)), -1, dtype=torch.int32, device=DEV)
+    out[:, :table.shape[1]] = table[:, :out.shape[1]]
+    return out if out.shape[1] > table.shape[1] else table
+
+
 def paged_check(lib, lens, page, hkv, group, D, dtype, seed=0, scale=None, edit=None, **kw):
-    cache, table, _, _ = fill(lib, lens, page, hkv, D, dtype, seed, edit)
+    cache, narrow, _, _ = fill(lib, lens, page, hkv, D, dtype, seed, edit)
     g = gen(seed + 100)
     row = normal(g, len(lens), hkv * group + 1, D)
     q = row[:, :hkv * group]
-    got = lib.paged_attention(q, cache, ints(lens), table, scale=scale, **kw)
-    lib.sync_status()
-    for s, n in enumerate(lens):
-        k, v = rows_of(cache, table, s, n)
-        see = torch.ones((1, n), dtype=torch.bool, device=DEV)
-        for h in range(hkv * group):
-            o, a = attend_clean(q[s:s + 1, h], k[:, h // group], v[:, h // group], see,
-                                D ** -0.5 if scale is None else scale)
-            close(got[s:s + 1, h], o, a, f"sequence {s} of {n}, head {h}")
+    for table in (narrow, widened(narrow, page, hkv)):
+        got = lib.paged_attention(q, cache, ints(lens), table, scale=scale, **kw)
+        lib.sync_status()
+        for s, n in enumerate(lens):
+            k, v = rows_of(cache, narrow, s, n)
+            see = torch.ones((1, n), dtype=torch.bool, device=DEV)
+            for h in range(hkv * group):
+                o, a = attend_clean(q[s:s + 1, h], k[:, h // group], v[:, h // group], see,
+                                    D ** -0.5 if scale is None else scale)
+                close(got[s:s + 1, h], o, a, f"sequence {s} of {n}, head {h}")
     return got
 
 
@@ -531,14 +542,17 @@ def test_paged_behind_the_length_does_not_leak(cuda_lib):
             close(got[s:s + 1, h], o, a)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("page", [16, 32, 128, 256, 1024])
-def test_paged_behind_the_length_and_bad_pages(cuda_lib, dtype, page):
+def test_paged_behind_the_length_and_bad_pages(cuda_lib, dtype, page, wide):
     """D = 128: what lies behind the length is not finite (scales too); then a page that
     is not there, a negative length and one beyond the page table: the rest is attended."""
     full, lens, D, group = [2 * page, 1040 + page, 5 * page], [page + 3, 1037, 4 * page + 1], 128, 4
     cache, table, _, _ = fill(cuda_lib, full, page, 1, D, dtype, seed=page)
     kept = [rows_of(cache, table, s, n) for s, n in enumerate(full)]
+    if wide:
+        table = widened(table, page, 1)
     for s, n in enumerate(lens):
         pos = torch.arange(n, full[s], device=DEV)
         at = table[s].long()[pos // page]
@@ -571,6 +585,8 @@ def test_paged_behind_the_length_and_bad_pages(cuda_lib, dtype, page):
     rest = torch.arange(lens[2], device=DEV)
     check(got, [torch.arange(page, lens[0], device=DEV), torch.arange(0, device=DEV),
                 rest[rest // page != 1]])
+    if wide:
+        return  # a length beyond a table this long would be over pages that are not there
     narrow = table[:, :1].contiguous()
     got = cuda_lib.paged_attention(q, cache, ints([page, page + 1, 2 ** 31 - 1]), narrow)
     with pytest.raises(cuda_lib.WanvaeError):
@@ -587,13 +603,15 @@ def test_paged_many_sequences_share_pages(cuda_lib, dtype, D, n):
     cache, table, _, _ = fill(cuda_lib, [70], page, 2, D, dtype, seed=n)
     lens = [(7 * i) % 71 for i in range(n)]
     q = normal(gen(n), n, 2 * group, D)
-    got = cuda_lib.paged_attention(q, cache, ints(lens), table.expand(n, -1).contiguous())
-    cuda_lib.sync_status()
     k, v = rows_of(cache, table, 0, 70)
     see = torch.arange(70, device=DEV)[None] < torch.tensor(lens, device=DEV)[:, None]
-    for h in range(2 * group):
-        o, a = attend_clean(q[:, h], k[:, h // group], v[:, h // group], see, D ** -0.5)
-        close(got[:, h], o, a, f"head {h}")
+    shared = table.expand(n, -1).contiguous()
+    for t in (shared, widened(shared, page, 2)):
+        got = cuda_lib.paged_attention(q, cache, ints(lens), t)
+        cuda_lib.sync_status()
+        for h in range(2 * group):
+            o, a = attend_clean(q[:, h], k[:, h // group], v[:, h // group], see, D ** -0.5)
+            close(got[:, h], o, a, f"head {h}")
     kk, vv = cuda_lib.kv_cache_gather(cache, table.expand(n, -1).contiguous(), starts(lens),
                                       total=sum(lens))
     cuda_lib.sync_status()
@@ -603,9 +621,12 @@ def test_paged_many_sequences_share_pages(cuda_lib, dtype, D, n):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
-def test_paged_query_not_finite(cuda_lib, dtype, bad):
+@pytest.mark.parametrize("wide", [False, True])
+def test_paged_query_not_finite(cuda_lib, dtype, bad, wide):
     """One head's query is not finite: that head's row is NaN, no other's."""
     cache, table, _, _ = fill(cuda_lib, [300, 40], 32, 2, 128, dtype, seed=4)
+    if wide:
+        table = widened(table, 32, 2)
     q = normal(gen(5), 2, 8, 128)
     clean = cuda_lib.paged_attention(q, cache, ints([300, 40]), table)
     q[0, 3, 17] = bad
@@ -617,11 +638,14 @@ def test_paged_query_not_finite(cuda_lib, dtype, bad):
     assert torch.equal(got[keep], clean[keep])
 
 
-@pytest.mark.parametrize("dtype,D", [(torch.float8_e4m3fn, 128), (torch.float8_e4m3fn, 64),
-                                     (torch.bfloat16, 128)])
-def test_paged_timeout_reports_and_context_survives(cuda_lib, dtype, D):
+@pytest.mark.parametrize("dtype,D,wide", [
+    (torch.float8_e4m3fn, 128, False), (torch.float8_e4m3fn, 128, True),
+    (torch.float8_e4m3fn, 64, False), (torch.bfloat16, 128, False)])
+def test_paged_timeout_reports_and_context_survives(cuda_lib, dtype, D, wide):
     lens = [3000, 17, 600]
     cache, table, _, _ = fill(cuda_lib, lens, 64, 2, D, dtype, seed=6)
+    if wide:
+        table = widened(table, 64, 2)
     q = normal(gen(6), 3, 8, D)
     want = cuda_lib.paged_attention(q, cache, ints(lens), table)
     cuda_lib.sync_status()
@@ -644,6 +668,7 @@ def test_paged_two_streams_at_once(cuda_lib, dtype):
     two streams: the results of calls one after another."""
     lens = [9000, 4000, 30]
     cache, table, _, _ = fill(cuda_lib, lens, 64, 2, 128, dtype, seed=8)
+    table = widened(table, 64, 2)
     qs = [normal(gen(i), 3, 8, 128) for i in range(2)]
     at = [ints(lens), ints([n // 2 for n in lens])]
     want = [cuda_lib.paged_attention(qs[i], cache, at[i], table) for i in range(2)]
@@ -812,8 +837,11 @@ def test_runs_repeat_bit_for_bit(cuda_lib):
     g = gen(4)
     q = normal(g, 3, 8, 128)
     a = [cuda_lib.paged_attention(q, cache, ints([3000, 40, 555]), table) for _ in range(3)]
+    wide = widened(table, 64, 2)
+    c = [cuda_lib.paged_attention(q, cache, ints([3000, 40, 555]), wide) for _ in range(3)]
     qkv = normal(g, 900, 6, 128)
     b = [cuda_lib.packed_attention(qkv[:, :4], qkv[:, 4:5], qkv[:, 5:], starts([500, 400]))
          for _ in range(3)]
     cuda_lib.sync_status()
-    assert all(torch.equal(a[0], t) for t in a) and all(torch.equal(b[0], t) for t in b)
+    for runs in (a, b, c):
+        assert all(torch.equal(runs[0], t) for t in runs)

@@ -27,17 +27,20 @@
 // the rows is chosen so that with TMA's swizzle eight lanes read eight banks' pieces
 // (rows of 128 bytes: column g of S is row g / 2 + 4 (g % 2)).
 //
-// 8-bit keys are multiplied as they are (an e4m3 MMA is four times the rate of a
-// 16-bit one, and needs no conversion): a query becomes two e4m3 terms, q 2^x =
-// a + b / 32 with a the nearest e4m3 value and b what is left, both exact for bf16's 8
-// bits down to 2^-14 of the query's largest element and within 2^-22 of it below
-// (x brings that element to exponent 7).  The second term takes the MMA's other
-// eight rows, which the heads leave free.  8-bit values become fp16 exactly, and
-// weights round once to fp16 (2^-12 relative): as two e4m3 terms small weights of
-// many rows would round alike.  A key row's scale multiplies its score; a value
-// row's scale 2^e joins the exponent of its weight, w_j = 2^(s_j + e_j - m) with m the
-// running maximum of s_j + e_j, while the sum takes 2^(s_j - m) in fp32, so that
-// weights stay in fp16's upper range whatever the scales are.
+// 8-bit elements become fp16, exactly, on their way into the MMA (mma.sync of e4m3 operands
+// has no rate of its own here).  A query is scaled by a power of two that brings its
+// largest element to exponent 14, where bf16's 8 bits stay whole down to 2^-31 of it
+// and below that round to within 2^-39 of it; weights round once to fp16 (2^-12
+// relative).  A key row's scale multiplies its score; a value row's scale 2^e joins the
+// exponent of its weight, w_j = 2^(s_j + e_j - m) with m the running maximum of s_j + e_j,
+// while the sum takes 2^(s_j - m) in fp32, so that weights stay in fp16's upper range
+// whatever the scales are.
+//
+// What bounds it: HBM for 16-bit rows (one sequence of 131040 rows, 8 kv heads of 8 query
+// heads of 128: 4.8 TB/s from a cold L2, 0.70 of the measured copy rate), the conversions
+// for 8-bit ones (the same in 8 bits: 60 us, 4.5 TB/s; about 470 warp instructions
+// for 16 rows of 128, half as many for 64).  Where a long 8-bit cache of 128-element heads
+// would wait for those, the tensor core reads it as it is: paged_attn_tc.cu.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -635,9 +638,19 @@ paged_join_kernel(const PagedArgs p, int block_heads) {
 
 int head_block(int G) { return G <= 8 ? 8 : 16; }
 
-// Whether a cache's rows go to the tcgen05 kernel: 8-bit rows of 128 elements, where
-// the tensor core takes the elements as they are (see paged_attn_tc.cu).
-bool on_tc(int D, bool e4m3) { return e4m3 && D == 128; }
+// Whether the tcgen05 kernel takes the call: 8-bit rows of 128 elements.  It reads faster but
+// begins an item later, and its threads' work grows with the query heads of a kv head.
+// Measured, here / there, in us, 8 kv heads: long tables, one sequence of 16384 rows 17.0 / 15.2
+// (4 query heads a kv head) and 18.1 / 18.9 (8), of 131040 58.6 / 48.7 and 60.2 / 52.0, 64
+// of 17 to 8192 122 / 89 and 135 / 113; short ones, 64 of 300 rows 23.4 / 28.9 and 29.1 /
+// 38.9, 64 of 1000 40.2 / 38.2 and 45.8 / 54.7, one of 300 8.2 / 10.9; 16 query heads,
+// one of 131040 68.4 / 79.8 (8 of them a turn there would read the cache twice).  The host
+// knows how far the page table reaches, not the lengths.
+bool on_tc(const KvCacheSpec &c, int G, int max_pages, int n_seq) {
+    const int64_t rows = (int64_t)max_pages << c.log2_page;
+    return c.e4m3 && c.D == 128 && G <= 8 && rows > 2048 &&
+           (rows + TcUnits::kRows - 1) / TcUnits::kRows * n_seq * c.H >= 512;
+}
 
 template <int D, class U>
 cudaError_t launch_join(const PagedArgs &a, int block_heads, const LaunchCtx &ctx) {
@@ -724,7 +737,7 @@ cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t 
     a.part_o = reinterpret_cast<float *>(a.part_ml + rows);
     a.err = ctx.err;
     a.wait_ns = ctx.wait_ns;
-    if (on_tc(c.D, c.e4m3)) {
+    if (on_tc(c, a.G, max_pages, n_seq)) {
         int heads = 0;
         const cudaError_t e = launch_paged_tc(a, c, ctx, &heads);
         return e != cudaSuccess ? e : launch_join<128, TcUnits>(a, heads, ctx);
@@ -733,8 +746,11 @@ cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t 
         if (c.e4m3) return hb == 8 ? launch<64, true, 1>(a, c, ctx) : launch<64, true, 2>(a, c, ctx);
         return hb == 8 ? launch<64, false, 1>(a, c, ctx) : launch<64, false, 2>(a, c, ctx);
     }
-    if (c.D == 128)
+    if (c.D == 128) {
+        if (c.e4m3)
+            return hb == 8 ? launch<128, true, 1>(a, c, ctx) : launch<128, true, 2>(a, c, ctx);
         return hb == 8 ? launch<128, false, 1>(a, c, ctx) : launch<128, false, 2>(a, c, ctx);
+    }
     return cudaErrorInvalidValue;
 }
 

@@ -154,7 +154,8 @@ __device__ __forceinline__ Cursor<U_> locate(const PagedArgs &p, int HH, int pla
 // The CTAs of a launch: as many as there can be units, at most `most`.
 int paged_ways(const PagedArgs &a, int rows, int most);
 
-// The tcgen05 kernel (paged_attn_tc.cu): 8-bit rows of 128 elements.  An item costs
+// The tcgen05 kernel (paged_attn_tc.cu): 8-bit rows of 128 elements, at most 8 query
+// heads a kv head.  An item costs
 // about what a unit does: the queries' way into shared memory, the first maximum,
 // the joined output.  *block_heads: the heads of a partial result.
 using TcUnits = Units<256, 1>;

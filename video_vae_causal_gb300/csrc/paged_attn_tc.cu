@@ -6,7 +6,7 @@
 // took about 470 warp instructions for every 16 rows, and was what bounded the
 // kernel.  Here the tensor core reads the elements as TMA left them in shared memory
 // (kind::f8f6f4), and the threads see scores and weights alone:
-//   S[row, col]  = K[row, :] . Qt[col, :]     128 rows, 16 or 32 columns
+//   S[row, col]  = K[row, :] . Qt[col, :]     128 rows, 16 columns
 //   Ot[d, col]  += sum_row V[row, d] Pt[col, row]
 // Both other operands become several e4m3 terms, each in columns of its own:
 //   a query, scaled by a power of two so that its largest element has exponent 7, is
@@ -32,6 +32,11 @@
 // where the product needs them, not before, so that most of the queue's bytes are in
 // flight.  What a unit is goes along with it in the queue, so only warp 8 knows the
 // split.  Every wait is bounded.
+//
+// What bounds it: HBM, behind what each item costs besides its units.  64 sequences of 17
+// to 8192 rows, 8 kv heads of 4 query heads: 94 us (5.7 TB/s, 0.84 of the measured copy
+// rate); one of 131040 rows, 8 heads of 8: 53 us (5.1 TB/s, 0.76; about 8 us of it
+// the launches, the first loads' latency and the join).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -65,14 +70,15 @@ struct Unit {
 // kLast alone where it has one), whether a range holds it whole, the end of all.
 enum : int { kFirst = 1, kSecond = 2, kLast = 4, kLastBut1 = 8, kWhole = 16, kEnd = 32 };
 
-// HP: query heads of an item, at most (4, 8 or 16).
+// HP: query heads of an item, at most (4 or 8: a thread's work grows with them, and
+// with 8 in place of 4 the sequences below take 113 us instead of 89).
 template <int HP>
 struct Cfg {
     static constexpr int N1 = 2 * HP < 16 ? 16 : 2 * HP;         // columns of S
     static constexpr int N2 = (3 * HP + 15) / 16 * 16;           // columns of O
     // Places for keys, which the scores free, and for values and what is told of a
     // unit, which the products free.
-    static constexpr int kKeys = 2, kStages = HP > 8 ? 3 : 4;
+    static constexpr int kKeys = 2, kStages = 4;
     static constexpr uint32_t kV = kKeys * kTileBytes;
     static constexpr uint32_t kP = kV + kStages * kTileBytes;    // [groups][halves][N2][128 rows]
     static constexpr uint32_t kPBytes = N2 * 128;
@@ -843,12 +849,9 @@ cudaError_t launch(PagedArgs &a, const KvCacheSpec &cache, const LaunchCtx &ctx)
 
 cudaError_t launch_paged_tc(PagedArgs &a, const KvCacheSpec &cache, const LaunchCtx &ctx,
                             int *block_heads) {
-    const int hp = a.G <= 4 ? 4 : a.G <= 8 ? 8 : 16;
-    a.HB = (a.G + hp - 1) / hp;
-    *block_heads = hp;
-    if (hp == 4) return launch<4>(a, cache, ctx);
-    if (hp == 8) return launch<8>(a, cache, ctx);
-    return launch<16>(a, cache, ctx);
+    a.HB = 1;
+    *block_heads = a.G <= 4 ? 4 : 8;
+    return a.G <= 4 ? launch<4>(a, cache, ctx) : launch<8>(a, cache, ctx);
 }
 
 }  // namespace wanvae
