@@ -17,6 +17,12 @@
 // neighbouring vectors; the loads of both tensors are in flight before the
 // first reduction.  Threads past the row's end hold zeros, so C need only be
 // a multiple of 16.
+//
+// Measured: 131040 tokens of 384 channels in bf16, a gate for every 6240 of them: 70 us,
+// 5.7 TB/s, 0.85 of the measured copy rate.  One resident wave of blocks that step through
+// the rows: a block for every 16 rows takes 80 us, five resident blocks in place of three
+// (fewer registers, fewer loads in flight) 77; streaming loads and stores change
+// nothing (70).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -15,13 +15,13 @@
 // Rows lie [page][head][slot][D]: the rows of one head and page are
 // contiguous, which is how attention over the cache reads them.  Both passes
 // move each row once (2 D bytes on one side, D + 1 on the other) and are bound
-// by HBM: 75000 tokens of 8 heads of 128 read back take 78 us (5.8 TB/s, 0.86 of
+// by HBM: 73513 tokens of 8 heads of 128 read back take 78 us (5.8 TB/s, 0.86 of
 // the measured copy rate), 16384 tokens written 27 us (3.7 TB/s, 0.55: a warp has
-// five tokens, whose places, loads and rows' maxima it waits for in turn; loading the next
-// pass's rows as each is used spilled and took 29 us).  A row takes D / 8 lanes with one 16-byte vector of bf16 each; a
-// warp keeps the rows of a token's heads together and takes tokens in a row, so
-// that a token's page is looked up once for all heads and its sequence once for the
-// tokens that follow it.
+// five tokens, whose places, loads and rows' maxima it waits for in turn; loading the
+// next pass's rows as each is used spilled and took 29 us).  A row takes D / 8 lanes with
+// one 16-byte vector of bf16 each; a warp keeps the rows of a token's heads together and
+// takes tokens in a row, so that a token's page is looked up once for all heads and its
+// sequence once for the tokens that follow it.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 256;
 // Rows of a lane's that are loaded before the first is used, and resident blocks that
-// leave the registers for them.  Sixteen prompts of 75000 tokens and 8 heads of 128
+// leave the registers for them.  Sixteen sequences, 73513 tokens of 8 heads of 128,
 // read back, in us: 8 rows and 3 blocks 81.7, 4 and 4 79.6, 4 and 5 77.7, 4 and 6 87
 // (spills), 2 and 6 82.3, 2 and 8 81.6.
 constexpr int kFlight = 4;
