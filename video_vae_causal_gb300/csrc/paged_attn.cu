@@ -10,7 +10,8 @@
 // Split.  The rows of one (sequence, kv head) are cut into units of 64 or 128; the
 // units of the whole batch, laid end to end, are dealt to the CTAs in equal
 // contiguous shares, so a ragged batch and a single long sequence load every
-// multiprocessor alike.  A share may begin or end inside an item: then its CTA
+// multiprocessor alike (behind short page tables each item is a CTA's own: kApartBytes).
+// A share may begin or end inside an item: then its CTA
 // leaves a partial result (the running maximum, the sum and the unnormalised output) in
 // the workspace, two slots a CTA, and a second small kernel joins them in the order of
 // the CTAs.  Which CTA left what follows from the lengths alone, so nothing is
@@ -56,6 +57,14 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kJoinThreads = 128;
+// Keys of an item (a sequence and a block of heads), as far as the page table reaches, up
+// to which a CTA takes an item whole and no join follows; twice this where a quarter of
+// the CTAs have one, four times where all have.  Shared / apart, in us, tables of 16-row
+// pages, 8-bit rows of 128: 8 items of 256 rows 8.2 / 6.1, of 512 8.3 / 8.6, of 1024 8.8 /
+// 13.8; 128 of 1024 20.0 / 18.8, of 2048 27.0 / 32.4; 320 of 1 to 2000 42.2 / 32.6, 512
+// 53.8 / 47.2, 1600 130 / 107; 16-bit rows of 128: 8 of 256 7.7 / 6.2, 128 of 512 17.6 / 13.5,
+// 512 of 1 to 1000 48.6 / 30.8.
+constexpr int64_t kApartBytes = 64 << 10;
 
 // D += A B, 16 x 8 x 16, fp16 or bf16 in, fp32 out.
 template <bool F16>
@@ -155,18 +164,33 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
     __syncthreads();
     griddep_wait();
     const int HH = p.H * p.HB;
-    const int total = S::U::before(p, p.n_seq, blockIdx.x == 0 && warp == 0) * HH;
-    const Split split(total, p.ways);
-    if ((int)blockIdx.x >= split.ways || total == 0) return;
+    Cursor<typename S::U> at;  // the unit to compute next
+    if (p.ways == 0) {         // an item a CTA
+        at.b = blockIdx.x / HH;
+        at.hh = blockIdx.x - at.b * HH;
+        at.u = 0;
+        at.len = seq_len(p, at.b, at.hh == 0 && warp == 0);
+        at.U = at.left = S::U::of(at.len);
+        if (at.len == 0) {
+            const int kvh = at.hh / p.HB, h0 = kvh * p.G + (at.hh % p.HB) * 8 * NH;
+            const int n = min(8 * NH, (kvh + 1) * p.G - h0) * D;
+            for (int e = threadIdx.x; e < n; e += kThreads)
+                p.out[(int64_t)at.b * p.out_stride + (int64_t)h0 * D + e] = __float2bfloat16(0.f);
+            return;
+        }
+    } else {
+        const int total = S::U::before(p, p.n_seq, blockIdx.x == 0 && warp == 0) * HH;
+        const Split split(total, p.ways);
+        if ((int)blockIdx.x >= split.ways || total == 0) return;
+        const int begin = split.begin(blockIdx.x);
+        at = locate<typename S::U>(p, HH, begin, split.begin(blockIdx.x + 1) - begin);
+    }
     const WaitCtl wc{p.wait_ns, p.err, abort_flag, 0u};
     bool ok = true;       // no wait of this warp has run out
     int fills = 0;        // turns copied, and the place in the queue of the next
     int put = 0, stage = 0;
     uint32_t phase = 0;   // of the turn to read next, at `stage`
 
-    const int begin = split.begin(blockIdx.x);
-    Cursor<typename S::U> at =  // the unit to compute next
-        locate<typename S::U>(p, HH, begin, split.begin(blockIdx.x + 1) - begin);
     // ---- copies, by lane 0: `ahead` is the unit to copy next, `page` its pages
     // (loaded one unit early), `kvh_ahead` its kv head
     Cursor<typename S::U> ahead = at;
@@ -640,7 +664,7 @@ int head_block(int G) { return G <= 8 ? 8 : 16; }
 
 // Whether the tcgen05 kernel takes the call: 8-bit rows of 128 elements.  It reads faster but
 // begins an item later, and its threads' work grows with the query heads of a kv head.
-// Measured, here / there, in us, 8 kv heads: long tables, one sequence of 16384 rows 17.0 / 15.2
+// Measured, here (in shares) / there, in us, 8 kv heads: long tables, one sequence of 16384 rows 17.0 / 15.2
 // (4 query heads a kv head) and 18.1 / 18.9 (8), of 131040 58.6 / 48.7 and 60.2 / 52.0, 64
 // of 17 to 8192 122 / 89 and 135 / 113; short ones, 64 of 300 rows 23.4 / 28.9 and 29.1 /
 // 38.9, 64 of 1000 40.2 / 38.2 and 45.8 / 54.7, one of 300 8.2 / 10.9; 16 query heads,
@@ -688,10 +712,15 @@ cudaError_t launch(PagedArgs a, const KvCacheSpec &cache, const LaunchCtx &ctx) 
         if (occ < 1) return cudaErrorInvalidConfiguration;
         per_sm[dev].store(occ, std::memory_order_release);
     }
-    a.ways = paged_ways(a, S::kUnit, std::min(kMaxWays, occ * ctx.num_sms));
+    const int most = std::min(kMaxWays, occ * ctx.num_sms);
+    const int64_t items = (int64_t)a.n_seq * a.H * a.HB;
+    const int64_t bytes = ((int64_t)a.max_pages << a.log2_page) * S::RB;
+    const bool apart = bytes <= kApartBytes * (items >= most ? 4 : 4 * items >= most ? 2 : 1);
+    a.ways = apart ? 0 : paged_ways(a, S::kUnit, most);
     count_launches(1);
-    e = launch_pdl(kern, dim3((unsigned)a.ways), dim3(kThreads), S::kSmem, ctx, mK, mV, a);
-    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3((unsigned)(apart ? items : a.ways)), dim3(kThreads), S::kSmem, ctx,
+                   mK, mV, a);
+    if (e != cudaSuccess || apart) return e;
     return launch_join<D, typename S::U>(a, 8 * NH, ctx);
 }
 

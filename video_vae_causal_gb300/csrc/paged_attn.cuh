@@ -27,7 +27,7 @@ struct PagedArgs {
     float scale_log2;
     __nv_bfloat16 *out;
     int64_t out_stride;
-    int ways;        // CTAs
+    int ways;        // CTAs that share the units; 0: an item a CTA
     float *part_o;   // [2 CTAs][heads of a block][D]
     float2 *part_ml; // [2 CTAs][heads of a block]: maximum, sum
     unsigned *err;
