@@ -37,10 +37,11 @@
 // while the sum takes 2^(s_j - m) in fp32, so that weights stay in fp16's upper range
 // whatever the scales are.
 //
-// What bounds it: HBM for 16-bit rows (one sequence of 131040 rows, 8 kv heads of 8 query
-// heads of 128: 4.8 TB/s from a cold L2, 0.70 of the measured copy rate), the conversions
-// for 8-bit ones (the same in 8 bits: 60 us, 4.5 TB/s; about 470 warp instructions
-// for 16 rows of 128, half as many for 64).  Where a long 8-bit cache of 128-element heads
+// What bounds it: HBM for 16-bit rows (64 sequences of 17 to 8192 rows, 8 kv heads of 4 query
+// heads of 128: 169 us, 6.1 TB/s, 0.90 of the measured copy rate; of 64: 89 us, 5.7 TB/s),
+// the conversions for 8-bit ones (of 64: 84 us, 3.0 TB/s; one sequence of 131040 rows, 8
+// heads of 8 of 128: 60 us, 4.5 TB/s; about 470 warp instructions for 16 rows of 128, half
+// as many for 64).  Where a long 8-bit cache of 128-element heads
 // would wait for those, the tensor core reads it as it is: paged_attn_tc.cu.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -105,7 +106,11 @@ struct Shape {
     static constexpr int NG = RB >= 256 ? 1 : 2;
     static constexpr int kCtas = 2;
     static constexpr int kUnit = 16 * NG * kWarps;   // cache rows of a unit
-    using U = Units<kUnit, 0>;
+    // An item's queries, first loads and join cost about two units: 32 sequences of 50 to
+    // 6000 rows, 4 kv heads, 16-bit rows of 128, take 45.2, 33.7 and 33.7 us with 0, 2 and
+    // 4 counted, 64 of 17 to 8192 rows, 8 kv heads, 174, 169 and 167 (8-bit rows of 64: 96,
+    // 84 and 88).
+    using U = Units<kUnit, 2>;
     static constexpr int kHalf = 16 * RB;            // bytes of a group's keys, or values
     static constexpr int kTurn = NG * 2 * kHalf;     // bytes of a warp's turn
     static constexpr int kRoom = (220 / kCtas - 2) * 1024 / (kWarps * kTurn);

@@ -225,9 +225,9 @@ wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
     if (!(scale > 0.f) || !(scale < INFINITY)) return WANVAE_ERR_INVALID_ARG;
     const size_t need = wanvae_paged_attention_workspace_size(n_heads, s.H, s.D);
     if (need == 0) return WANVAE_ERR_UNSUPPORTED;
-    // rows of a sequence, and units of 64 rows that the page table could hold (one more
+    // rows of a sequence, and units of 64 rows that the page table could hold (two more
     // an item, an item for each kv head and 8 query heads), are counted in 32 bits
-    const int64_t units = ((max_pages << s.log2_page) + 63) / 64 + 1;
+    const int64_t units = ((max_pages << s.log2_page) + 63) / 64 + 2;
     const int64_t items = n_seq * s.H * ((n_heads / s.H + 7) / 8);
     if (units > INT32_MAX / 256 || units * items > INT32_MAX) return WANVAE_ERR_UNSUPPORTED;
     const int64_t w = n_heads * s.D;
