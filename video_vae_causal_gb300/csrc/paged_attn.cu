@@ -671,7 +671,7 @@ int head_block(int G) { return G <= 8 ? 8 : 16; }
 // begins an item later, and its threads' work grows with the query heads of a kv head.
 // Measured, here (in shares) / there, in us, 8 kv heads: long tables, one sequence of 16384 rows 17.0 / 15.2
 // (4 query heads a kv head) and 18.1 / 18.9 (8), of 131040 58.6 / 48.7 and 60.2 / 52.0, 64
-// of 17 to 8192 122 / 89 and 135 / 113; short ones, 64 of 300 rows 23.4 / 28.9 and 29.1 /
+// of 17 to 8192 122 / 89 and 135 / 104; short ones, 64 of 300 rows 23.4 / 28.9 and 29.1 /
 // 38.9, 64 of 1000 40.2 / 38.2 and 45.8 / 54.7, one of 300 8.2 / 10.9; 16 query heads,
 // one of 131040 68.4 / 79.8 (8 of them a turn there would read the cache twice).  The host
 // knows how far the page table reaches, not the lengths.

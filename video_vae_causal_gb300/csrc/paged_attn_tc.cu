@@ -71,7 +71,7 @@ struct Unit {
 enum : int { kFirst = 1, kSecond = 2, kLast = 4, kLastBut1 = 8, kWhole = 16, kEnd = 32 };
 
 // HP: query heads of an item, at most (4 or 8: a thread's work grows with them, and
-// with 8 in place of 4 the sequences below take 113 us instead of 89).
+// with 8 in place of 4 the sequences below take 104 us instead of 89).
 template <int HP>
 struct Cfg {
     static constexpr int N1 = 2 * HP < 16 ? 16 : 2 * HP;         // columns of S
