@@ -1,0 +1,71 @@
+"""The 8-bit key-value cache over the whole range of its scales: rows near the largest
+finite value, rows whose scales lie further apart than fp32's exponents reach, rows of
+zeros.  References, bounds and inputs as in test_seq_gpu.py; every case runs behind a
+page table as long as the sequences and behind one that reaches further, which are
+different kernels for 128-element heads."""
+import math
+
+import pytest
+import torch
+
+import test_seq_gpu as seq
+from test_seq_gpu import DEV, close, fill, gen, ints, normal, rows_of, widened
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+BF16_MAX = torch.finfo(torch.bfloat16).max
+
+
+def attended(lib, cache, narrow, lens, q, group, scale, what=""):
+    """paged_attention behind both tables against the cache's rows in 64 bits; what lies
+    beyond bf16's finite values saturates."""
+    hkv = cache.heads
+    for table in (narrow, widened(narrow, cache.page_size, hkv)):
+        got = lib.paged_attention(q, cache, ints(lens), table, scale=scale)
+        lib.sync_status()
+        for s, n in enumerate(lens):
+            k, v = rows_of(cache, narrow, s, n)
+            see = torch.ones((1, n), dtype=torch.bool, device=DEV)
+            for h in range(hkv * group):
+                o, a = seq.attend_clean(q[s:s + 1, h], k[:, h // group], v[:, h // group], see,
+                                        scale)
+                close(got[s:s + 1, h], o.clamp(-BF16_MAX, BF16_MAX), a,
+                      f"{what} sequence {s} of {n}, head {h}")
+    return got
+
+
+HEADS = [(64, 4), (64, 12), (128, 4), (128, 8), (128, 12)]
+
+
+@pytest.mark.parametrize("D,group", HEADS)
+def test_paged_values_near_the_largest(cuda_lib, D, group):
+    """Value rows of up to 1.9 * 2^127: scales of 2^120, so that a weight that carries its
+    row's scale and the sum of the weights without scales are 2^120 apart."""
+    lens, scale = [3000, 300, 1], 1.5 * D ** -0.5
+
+    def edit(k, v):
+        v[:] = normal(gen(11), *v.shape) * 2.0 ** 125
+        v[:, :, 0] = 1.9 * 2.0 ** 127
+        v[::2, :, 0] *= -1
+    cache, table, _, _ = fill(cuda_lib, lens, 64, 1, D, E4M3, seed=D + group, edit=edit)
+    assert torch.all(cache.v_exp.view(torch.uint8)[table[0, 0]] == 247)
+    attended(cuda_lib, cache, table, lens, normal(gen(1), 3, group, D), group, scale)
+
+
+@pytest.mark.parametrize("D,group", HEADS)
+@pytest.mark.parametrize("order", ["mixed", "rising", "falling"])
+def test_paged_value_scales_beyond_fp32(cuda_lib, D, group, order):
+    """Half of the value rows are 2^160 times the others: the small ones add nothing to the
+    output, but their weights count in its denominator."""
+    lens, scale = [2000, 130], D ** -0.5
+
+    def edit(k, v):
+        at = 0
+        for n in lens:
+            i = torch.arange(n, device=DEV)
+            big = {"mixed": i % 2 == 0, "rising": i >= n // 2, "falling": i < n // 2}[order]
+            v[at:at + n] *= torch.where(big, 2.0 ** 100, 2.0 ** -60)[:, None, None]
+            at += n
+    cache, table, _, _ = fill(cuda_lib, lens, 32, 1, D, E4M3, seed=D + group, edit=edit)
+    attended(cuda_lib, cache, table, lens, normal(gen(2), 2, group, D), group, scale, order)

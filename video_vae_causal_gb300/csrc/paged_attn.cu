@@ -34,8 +34,8 @@
 // and below that round to within 2^-39 of it; weights round once to fp16 (2^-12
 // relative).  A key row's scale multiplies its score; a value row's scale 2^e joins the
 // exponent of its weight, w_j = 2^(s_j + e_j - m) with m the running maximum of s_j + e_j,
-// while the sum takes 2^(s_j - m) in fp32, so that weights stay in fp16's upper range
-// whatever the scales are.
+// so that weights stay in fp16's upper range whatever the scales are, while the sum takes
+// 2^(s_j - r) in fp32, r the running maximum of the scores alone (see paged_attn.cuh).
 //
 // What bounds it: HBM for 16-bit rows (64 sequences of 17 to 8192 rows, 8 kv heads of 4 query
 // heads of 128: 169 us, 6.1 TB/s, 0.90 of the measured copy rate; of 64: 89 us, 5.7 TB/s),
@@ -119,7 +119,7 @@ struct Shape {
     static constexpr int kBarOff = kExpOff + kStages * kWarps * NG * 32;
     static constexpr int kMetaOff = kBarOff + kStages * kWarps * 8;
     static constexpr int kMlOff = kMetaOff + kStages * kWarps * 4;
-    static constexpr int kAbortOff = kMlOff + kWarps * NH * 8 * 8;
+    static constexpr int kAbortOff = kMlOff + kWarps * NH * 8 * 16;
     static constexpr int kSmem = 1024 + kAbortOff + 16;
     static_assert(kStages >= 2, "queue");
     // A warp's outputs wait for the join in its part of the turn just read:
@@ -301,11 +301,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                                  : raw[s].y;
             }
         }
-        float m[NH], l[NH];  // of head g + 8 i; the sum over this thread's rows alone
+        // of head g + 8 i; the sum, and r of an 8-bit cache, of this thread's rows alone
+        float m[NH], r[NH], l[NH];
         float o[NH][kSteps][4];
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
-            m[i] = -INFINITY;
+            m[i] = r[i] = kLowest;
             l[i] = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
@@ -410,9 +411,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                 // their sums below fp16's products' fp32 range, and O is seldom rescaled
                 if (__any_sync(0xffffffffu, mx > m[h] + 4.f)) {
                     const float mn = fmaxf(m[h], mx);
-                    const float f = mn == -INFINITY ? 0.f : exp2_fast(m[h] - mn);
+                    const float f = exp2_fast(m[h] - mn);
                     m[h] = mn;
-                    l[h] *= f;
+                    if (!Q8) l[h] *= f;
                     const float f0 = __shfl_sync(0xffffffffu, f, 8 * t);
                     const float f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
@@ -423,7 +424,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                         o[h][k][3] *= f1;
                     }
                 }
-                const float ms = m[h] == -INFINITY ? 0.f : m[h];  // nothing seen yet: weights 0
+                if (Q8) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) top = max3(top, s[i][j][0], s[i][j][1]);
+                    raise_sum(top, kSumLag, r[h], l[h]);
+                }
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
                     float w[2][2];
@@ -431,10 +439,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const float x = s[i][j][c] - ms;
-                            const float e = exp2_fast(x);
+                            const float e = exp2_fast(s[i][j][c] - (Q8 ? r[h] : m[h]));
                             l[h] += e;
-                            w[j][c] = Q8 ? exp2_fast(x + ve[i][j][c]) : e;
+                            w[j][c] = Q8 ? exp2_fast(s[i][j][c] + (ve[i][j][c] - m[h])) : e;
                         }
                     pb[h][i][0] = pack16<Q8>(w[0][0], w[0][1]);
                     pb[h][i][1] = pack16<Q8>(w[1][0], w[1][1]);
@@ -519,13 +526,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
         // outputs go to the turn that it has just read (the next copy into it comes
         // after the second barrier).
         const int last = (stage == 0 ? S::kStages : stage) - 1;
-        float2 *ml = reinterpret_cast<float2 *>(smem + S::kMlOff);
+        float4 *ml = reinterpret_cast<float4 *>(smem + S::kMlOff);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
+            if (Q8) {
+                float top = fmaxf(r[i], __shfl_xor_sync(0xffffffffu, r[i], 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                l[i] *= exp2_fast(r[i] - top);
+                r[i] = top;
+            }
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (t == 0) ml[(warp * NH + i) * 8 + g] = make_float2(m[i], l[i]);
+            if (t == 0)
+                ml[(warp * NH + i) * 8 + g] = make_float4(m[i], Q8 ? r[i] : 0.f, l[i], 0.f);
             float *dst = reinterpret_cast<float *>(turns + last * S::kTurn) + i * S::kJoinHeads;
             constexpr int kEl = S::VB / S::EB;  // elements of a value piece
 #pragma unroll
@@ -543,27 +557,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
         for (int e = threadIdx.x; e < heads * D; e += kThreads) {
             const int h = e / D, d = e % D;
             const int i = h >> 3, hr = h & 7;
-            float mw[kWarps], top = -INFINITY;
+            float4 mw[kWarps];
+            float top = kLowest, rtop = kLowest;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                mw[w] = ml[(w * NH + i) * 8 + hr].x;
-                top = fmaxf(top, mw[w]);
+                mw[w] = ml[(w * NH + i) * 8 + hr];
+                top = fmaxf(top, mw[w].x);
+                if (Q8) rtop = fmaxf(rtop, mw[w].y);
             }
             float sum = 0.f, acc = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = mw[w] == -INFINITY ? 0.f : exp2_fast(mw[w] - top);
-                sum += f * ml[(w * NH + i) * 8 + hr].y;
+                const float f = exp2_fast(mw[w].x - top);
+                sum += (Q8 ? exp2_fast(mw[w].y - rtop) : f) * mw[w].z;
                 acc += f * reinterpret_cast<const float *>(
                                smem + (w * S::kStages + last) * S::kTurn)
                                [i * S::kJoinHeads + d * 8 + (d >> 4) * S::kPad + hr];
             }
             if (whole) {
                 p.out[(int64_t)at.b * p.out_stride + (int64_t)(h0 + h) * D + d] =
-                    __float2bfloat16(sum > 0.f || sum != sum ? acc / sum : 0.f);
+                    __float2bfloat16(output_of<Q8>(acc, sum, top, rtop));
             } else {
                 p.part_o[((int64_t)slot * (8 * NH) + h) * D + d] = acc;
-                if (d == 0) p.part_ml[slot * (8 * NH) + h] = make_float2(top, sum);
+                if (d == 0) p.part_ml[slot * (8 * NH) + h] = make_float4(top, rtop, sum, 0.f);
             }
         }
         fence_proxy_async_smem();  // the buffers' next writer is the TMA
@@ -583,12 +599,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
 // Joins the partial results of the items that were cut between CTAs, and
 // writes zeros for sequences without rows.  One block for each (query head,
 // sequence): the parts' weights side by side, then a warp for every fourth part.
-template <int D, class U>
+template <int D, bool Q8, class U>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const PagedArgs p, int block_heads) {
     constexpr int kW = kJoinThreads / 32, E = D / 32;
     __shared__ float weight[kMaxWays];
-    __shared__ float2 warp_ml[kW];
+    __shared__ float warp_m[kW], warp_r[kW], warp_l[kW];
     __shared__ float acc_w[kW][D];
     griddep_launch_dependents();
     griddep_wait();
@@ -610,24 +626,37 @@ paged_join_kernel(const PagedArgs p, int block_heads) {
     // the item lies in the first slot of its CTAs, but for one with units before it
     const int s0 = 2 * w0 + (split.begin(w0) < i0 ? 1 : 0);
     auto slot_of = [&](int i) { return (i == 0 ? s0 : 2 * (w0 + i)) * block_heads + hr; };
-    float top = -INFINITY;
-    for (int i = tid; i < n; i += kJoinThreads) top = fmaxf(top, p.part_ml[slot_of(i)].x);
+    float top = kLowest, rtop = kLowest;
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const float4 ml = p.part_ml[slot_of(i)];
+        top = fmaxf(top, ml.x);
+        if (Q8) rtop = fmaxf(rtop, ml.y);
+    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane == 0) warp_ml[warp].x = top;
+    for (int off = 16; off > 0; off >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        if (Q8) rtop = fmaxf(rtop, __shfl_xor_sync(0xffffffffu, rtop, off));
+    }
+    if (lane == 0) {
+        warp_m[warp] = top;
+        if (Q8) warp_r[warp] = rtop;
+    }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kW; ++w) top = fmaxf(top, warp_ml[w].x);
+    for (int w = 0; w < kW; ++w) {
+        top = fmaxf(top, warp_m[w]);
+        if (Q8) rtop = fmaxf(rtop, warp_r[w]);
+    }
     float sum = 0.f;
     for (int i = tid; i < n; i += kJoinThreads) {
-        const float2 ml = p.part_ml[slot_of(i)];
-        const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+        const float4 ml = p.part_ml[slot_of(i)];
+        const float f = exp2_fast(ml.x - top);
         weight[i] = f;
-        sum += f * ml.y;
+        sum += (Q8 ? exp2_fast(ml.y - rtop) : f) * ml.z;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) warp_ml[warp].y = sum;
+    if (lane == 0) warp_l[warp] = sum;
     __syncthreads();
     float acc[E] = {};
     constexpr int kBatch = 8;  // loads in flight
@@ -659,9 +688,9 @@ paged_join_kernel(const PagedArgs p, int block_heads) {
 #pragma unroll
         for (int w = 0; w < kW; ++w) {
             a += acc_w[w][tid];
-            sum += warp_ml[w].y;
+            sum += warp_l[w];
         }
-        out[tid] = __float2bfloat16(sum > 0.f || sum != sum ? a / sum : 0.f);
+        out[tid] = __float2bfloat16(output_of<Q8>(a, sum, top, rtop));
     }
 }
 
@@ -681,10 +710,10 @@ bool on_tc(const KvCacheSpec &c, int G, int max_pages, int n_seq) {
            (rows + TcUnits::kRows - 1) / TcUnits::kRows * n_seq * c.H >= 512;
 }
 
-template <int D, class U>
+template <int D, bool Q8, class U>
 cudaError_t launch_join(const PagedArgs &a, int block_heads, const LaunchCtx &ctx) {
     count_launches(1);
-    return launch_pdl(paged_join_kernel<D, U>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
+    return launch_pdl(paged_join_kernel<D, Q8, U>, dim3((unsigned)(a.H * a.G), (unsigned)a.n_seq),
                       dim3(kJoinThreads), 0, ctx, a, block_heads);
 }
 
@@ -726,7 +755,7 @@ cudaError_t launch(PagedArgs a, const KvCacheSpec &cache, const LaunchCtx &ctx) 
     e = launch_pdl(kern, dim3((unsigned)(apart ? items : a.ways)), dim3(kThreads), S::kSmem, ctx,
                    mK, mV, a);
     if (e != cudaSuccess || apart) return e;
-    return launch_join<D, typename S::U>(a, 8 * NH, ctx);
+    return launch_join<D, Q8, typename S::U>(a, 8 * NH, ctx);
 }
 
 }  // namespace
@@ -737,10 +766,10 @@ int paged_ways(const PagedArgs &a, int rows, int most) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(units, most));
 }
 
-// The parts' maxima and sums, then their outputs.
+// The parts' references and sums, then their outputs.
 size_t paged_attention_workspace(int Hq, int Hkv, int D) {
     const size_t rows = (size_t)2 * kMaxWays * head_block(Hq / Hkv);
-    return rows * (D * sizeof(float) + sizeof(float2));
+    return rows * (D * sizeof(float) + sizeof(float4));
 }
 
 cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t q_stride,
@@ -767,14 +796,14 @@ cudaError_t launch_paged_attention(const KvCacheSpec &c, const void *q, int64_t 
     a.out_stride = out_stride;
     const size_t rows = (size_t)2 * kMaxWays * hb;
     a.ways = 0;
-    a.part_ml = static_cast<float2 *>(workspace);
+    a.part_ml = static_cast<float4 *>(workspace);
     a.part_o = reinterpret_cast<float *>(a.part_ml + rows);
     a.err = ctx.err;
     a.wait_ns = ctx.wait_ns;
     if (on_tc(c, a.G, max_pages, n_seq)) {
         int heads = 0;
         const cudaError_t e = launch_paged_tc(a, c, ctx, &heads);
-        return e != cudaSuccess ? e : launch_join<128, TcUnits>(a, heads, ctx);
+        return e != cudaSuccess ? e : launch_join<128, true, TcUnits>(a, heads, ctx);
     }
     if (c.D == 64) {
         if (c.e4m3) return hb == 8 ? launch<64, true, 1>(a, c, ctx) : launch<64, true, 2>(a, c, ctx);

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -29,7 +30,7 @@ struct PagedArgs {
     int64_t out_stride;
     int ways;        // CTAs that share the units; 0: an item a CTA
     float *part_o;   // [2 CTAs][heads of a block][D]
-    float2 *part_ml; // [2 CTAs][heads of a block]: maximum, sum
+    float4 *part_ml; // [2 CTAs][heads of a block]: m and r (below; 8 bits alone), sum
     unsigned *err;
     uint64_t wait_ns;
 };
@@ -149,6 +150,36 @@ __device__ __forceinline__ Cursor<U_> locate(const PagedArgs &p, int HH, int pla
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
     return at;
+}
+
+// Two references in log2 units belong to a head's output and sum: m, a little below or at the
+// largest s + e (a row's score, and the exponent of its value row's scale), which the
+// output's weights 2^(s + e - m) are relative to, and r, at most kSumLag below the largest s
+// and never above it, for the sum of 2^(s - r).  One reference for both would not do: scales
+// reach from 2^-100 to 2^120, and a sum relative to m lost every row more than 2^6 below the
+// largest under scales of 2^120, or all rows but some where scales lie 2^126 apart.  Both
+// begin at kLowest, which any score passes.
+constexpr float kLowest = -FLT_MAX;
+constexpr float kSumLag = 60.f;  // (2^31 rows of 2^60 stay in fp32's range)
+
+// The output from sums relative to m and r, zero where no row counted: acc / sum *
+// 2^(m - r), this last in two factors, as m - r is up to 120 + kSumLag.  (Rows of 16 bits have
+// no scales, and one reference.)
+__device__ __forceinline__ float half_factor(float m, float r) { return exp2_fast(0.5f * (m - r)); }
+template <bool Q8>
+__device__ __forceinline__ float output_of(float acc, float sum, float m, float r) {
+    const float o = sum > 0.f || sum != sum ? acc / sum : 0.f;
+    if (!Q8) return o;
+    const float f = half_factor(m, r);
+    return o * f * f;
+}
+
+// Moves r, and the sum l with it, where `top` lies more than `lag` above it.
+__device__ __forceinline__ void raise_sum(float top, float lag, float &r, float &l) {
+    if (top > r + lag) {
+        l *= exp2_fast(r - top);
+        r = top;
+    }
 }
 
 // The CTAs of a launch: as many as there can be units, at most `most`.

@@ -16,7 +16,8 @@
 //   largest weight where that is more (as fp16 would hold it).
 // A key row's scale multiplies its score; a value row's scale 2^e joins the exponent
 // of its weight, w = 2^(s + e - m), with m the running maximum of s + e, while the sum
-// takes 2^(s - m) in fp32.  m moves only by more than 1, so weights stay below 2.
+// takes 2^(s - r) in fp32, r that of s alone (see paged_attn.cuh).  m moves only by more
+// than 1, so weights stay below 2.
 //
 // A unit is 256 rows, two MMAs' worth: each role's waits and bookkeeping take it about
 // 1000 cycles a unit, whatever its size.
@@ -70,6 +71,13 @@ struct Unit {
 // kLast alone where it has one), whether a range holds it whole, the end of all.
 enum : int { kFirst = 1, kSecond = 2, kLast = 4, kLastBut1 = 8, kWhole = 16, kEnd = 32 };
 
+// What a softmax warp keeps for the heads of its item, in shared memory (own[kind + head]):
+// the queries' factors; the largest s + e where m moves; m and r (paged_attn.cuh; m is the
+// group's, r the warp's); the factors that O and the sums go on with; the sum at the item's
+// end and its r.  (Other warps read the fourth kind no more: a warp may have begun the next item.)
+enum : int { kOwnQs = 0, kOwnTop = 8, kOwnM = 16, kOwnR = 24, kOwnF = 32, kOwnFl = 40, kOwnL = 48,
+             kOwnRl = 56, kOwnSize = 64 };
+
 // HP: query heads of an item, at most (4 or 8: a thread's work grows with them, and
 // with 8 in place of 4 the sequences below take 104 us instead of 89).
 template <int HP>
@@ -88,9 +96,9 @@ struct Cfg {
     static constexpr uint32_t kMeta = kExp + kStages * 2 * kUnit;
     static constexpr uint32_t kPages = kMeta + kStages * sizeof(Unit);  // [stages][page, row]
     static constexpr uint32_t kQs = kPages + kStages * kBoxes * 8;  // [2][16] floats
-    static constexpr uint32_t kRed = kQs + 128;                  // [groups][2][4][16] floats
-    static constexpr uint32_t kJoin = kRed + 1024;               // [HP][128 + maximum, sum]
-    static constexpr uint32_t kBars = kJoin + HP * 130 * 4;
+    static constexpr uint32_t kOwn = kQs + 128;                  // [8 warps][kOwnSize] floats
+    static constexpr uint32_t kJoin = kOwn + 8 * kOwnSize * 4;         // [HP][128], [HP][m, r, sum, -]
+    static constexpr uint32_t kBars = kJoin + HP * 132 * 4;
     static constexpr uint32_t kSlots = kBars + 8 * (2 * kKeys + 4 * kStages + 20);
     static constexpr uint32_t kSmem = 1024 + kSlots + 16;
     // TMEM: S of half h of units i % 4 at columns 64 (i % 4) + 32 h, then each group's O
@@ -186,10 +194,11 @@ __device__ __forceinline__ void bar_group(int w) {
     asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
 }
 
+// The largest of a warp (a NaN loses to a number).
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
@@ -507,19 +516,55 @@ __device__ void issue_products(uint8_t *smem, uint32_t tmem, const Bars<HP> &bar
     drain_mmas(bars.drain(1), wc);
 }
 
+template <int HP>
+__device__ __forceinline__ void read_own(const float *own, float (&v)[HP]) {
+#pragma unroll
+    for (int h = 0; h < HP; h += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(own + h);
+        v[h] = x.x;
+        v[h + 1] = x.y;
+        v[h + 2] = x.z;
+        v[h + 3] = x.w;
+    }
+}
+
+// The sum over the warp of v[h], in the lanes h, h + HP, ..
+template <int HP>
+__device__ __forceinline__ float warp_sums(float (&v)[HP], int lane) {
+#pragma unroll
+    for (int b = HP / 2; b > 0; b >>= 1) {
+        const bool up = (lane & b) != 0;
+#pragma unroll
+        for (int j = 0; j < b; ++j) {
+            const float give = up ? v[j] : v[j + b];
+            v[j] = (up ? v[j + b] : v[j]) + __shfl_xor_sync(0xffffffffu, give, b);
+        }
+    }
+#pragma unroll
+    for (int off = HP; off < 32; off <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    return v[0];
+}
+
 // Group w (warps 4 w .. 4 w + 3): every second unit.  Thread r: rows r and r + 128 of a
 // unit, and element r of the outputs.  A warp whose wait runs out does no more work, but keeps
 // to the group's barriers until all four learn of it and leave together.
+//
+// What a head needs once in a while -- moving m and r, joining the warps' sums and the groups'
+// outputs -- is done by one lane for each head: a single long sequence passes through
+// here a few times only, and what it waits for is the instructions themselves (all heads'
+// worth in every thread: 57 us in place of 53 for 131040 rows, 8 heads of 8).
 template <int HP>
 __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
                         const Bars<HP> &bars, const WaitCtl &wc) {
     using C = Cfg<HP>;
     const int r = threadIdx.x & 127, warp = r >> 5, lane = r & 31;
+    const int hl = lane & (HP - 1);  // this lane's head
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t to = trow + C::o_col(w);
     const Unit *queue = reinterpret_cast<const Unit *>(smem + C::kMeta);
-    float *red = reinterpret_cast<float *>(smem + C::kRed) + w * 128;
-    float *join = reinterpret_cast<float *>(smem + C::kJoin);
+    float *group = reinterpret_cast<float *>(smem + C::kOwn) + w * 4 * kOwnSize;
+    float *own = group + warp * kOwnSize;
+    float *join = reinterpret_cast<float *>(smem + C::kJoin), *join_stat = join + HP * 128;
     // the place of this row in P's rows n (128-byte swizzle)
     uint32_t place[8];
 #pragma unroll
@@ -530,9 +575,12 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
     buf.i = w;
     Turn<1> turn, joins;  // parities alone
     const int log2_box = min(p.log2_page, 7);
-    float qs[HP], m[HP], l[HP], s[kHalves][HP];
+    float m[HP], l[HP], s[kHalves][HP];
 #pragma unroll
-    for (int h = 0; h < HP; ++h) qs[h] = m[h] = l[h] = s[0][h] = s[kHalves - 1][h] = 0.f;
+    for (int h = 0; h < HP; ++h) m[h] = l[h] = s[0][h] = s[kHalves - 1][h] = 0.f;
+    // While the rows' e are at least this, no s is more than kSumLag above its r, as no
+    // s + e is more than m + 1: one comparison a row stands for those of all heads.
+    float least_e = INFINITY;
     bool ok = true;
     while (true) {
         ok = ok && mbar_wait_warp<false>(bars.told(get.i), get.phase, wc);
@@ -545,12 +593,17 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
             if (fresh) {
                 const int q = u.item & 1;
                 ok = mbar_wait_warp<false>(bars.q_ready(q), (uint32_t)(u.item >> 1) & 1u, wc);
+                __syncwarp();
+                if (lane < HP) {
+                    own[kOwnQs + lane] = reinterpret_cast<const float *>(smem + C::kQs)[q * 16 + lane];
+                    own[kOwnM + lane] = own[kOwnR + lane] = kLowest;
+                }
 #pragma unroll
                 for (int h = 0; h < HP; ++h) {
-                    qs[h] = reinterpret_cast<const float *>(smem + C::kQs)[q * 16 + h];
-                    m[h] = -INFINITY;
+                    m[h] = kLowest;
                     l[h] = 0.f;
                 }
+                least_e = INFINITY;
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bars.q_free(q));
@@ -562,6 +615,8 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
         }
         if (ok && !end) {
             tc_fence_after();
+            float qs[HP];
+            read_own<HP>(own + kOwnQs, qs);
 #pragma unroll
             for (int k = 0; k < kHalves; ++k) {
                 const int row = k * 128 + r;
@@ -569,6 +624,7 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
                 const float kf = __uint_as_float((uint32_t)ex[0] << 23);
                 ve[k] = (float)ex[kUnit] - 127.f;
                 there[k] = row < u.rows && !((u.missing >> (row >> log2_box)) & 1u);
+                moves |= ve[k] < least_e;
                 uint32_t raw[C::N1];
                 tmem_read(trow + C::s_col(buf.i) + 32u * k, raw);
                 // scores in log2 units
@@ -589,26 +645,47 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
         if (bar_any(1 + w, 128, moves || !ok)) {
             if (bar_any(1 + w, 128, !ok)) return;
             if (!end) {
-                float f[HP];
+                float top = -INFINITY, stop = -INFINITY;  // of s + e, of s; head hl's
 #pragma unroll
                 for (int h = 0; h < HP; ++h) {
-                    float top = s[0][h] + ve[0];
+                    float x = s[0][h], y = s[0][h] + ve[0];
 #pragma unroll
-                    for (int k = 1; k < kHalves; ++k) top = fmaxf(top, s[k][h] + ve[k]);
-                    top = warp_max(top);
-                    if (lane == 0) red[warp * 16 + h] = top;
+                    for (int k = 1; k < kHalves; ++k) {
+                        x = fmaxf(x, s[k][h]);
+                        y = fmaxf(y, s[k][h] + ve[k]);
+                    }
+                    x = warp_max(x);
+                    y = warp_max(y);
+                    if (hl == h) {
+                        stop = x;
+                        top = y;
+                    }
                 }
+                if (lane < HP) own[kOwnTop + lane] = top;
                 bar_group(w);
+                float e = -INFINITY;
+                if (lane < HP) {
+                    const float m0 = own[kOwnM + lane], r0 = own[kOwnR + lane];
+                    float mn = m0;
 #pragma unroll
-                for (int h = 0; h < HP; ++h) {
-                    float mn = m[h];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mn = fmaxf(mn, red[k * 16 + h]);
-                    f[h] = mn == -INFINITY ? 0.f : exp2_fast(m[h] - mn);
-                    m[h] = mn;
-                    l[h] *= f[h];
+                    for (int k = 0; k < 4; ++k)
+                        mn = fmaxf(mn, group[k * kOwnSize + kOwnTop + lane]);
+                    const float rn = fmaxf(r0, stop);
+                    own[kOwnM + lane] = mn;
+                    own[kOwnR + lane] = rn;
+                    own[kOwnF + lane] = exp2_fast(m0 - mn);
+                    own[kOwnFl + lane] = exp2_fast(r0 - rn);
+                    e = mn - rn - (kSumLag - 1.f);
                 }
+                least_e = warp_max(e);
+                __syncwarp();
+                float f[HP];
+                read_own<HP>(own + kOwnFl, f);
+#pragma unroll
+                for (int h = 0; h < HP; ++h) l[h] *= f[h];
+                read_own<HP>(own + kOwnM, m);
                 if (!fresh) {
+                    read_own<HP>(own + kOwnF, f);
                     tc_fence_after();
                     uint32_t o[C::N2];
                     tmem_read(to, o);
@@ -624,6 +701,8 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
         }
         if (end) return;
         // weights, times 2^7, as three terms
+        float rs[HP];
+        read_own<HP>(own + kOwnR, rs);
 #pragma unroll
         for (int k = 0; k < kHalves; ++k) {
             uint8_t *pb = smem + C::kP + (w * kHalves + k) * C::kPBytes;
@@ -632,10 +711,8 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
                 float x[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float ms = m[h + c] == -INFINITY ? 0.f : m[h + c];
-                    const float y = s[k][h + c] - ms;
-                    l[h + c] += exp2_fast(y);
-                    x[c] = exp2_fast(y + (ve[k] + 7.f));
+                    l[h + c] += exp2_fast(s[k][h + c] - rs[h + c]);
+                    x[c] = exp2_fast(s[k][h + c] + ((ve[k] + 7.f) - m[h + c]));
                 }
 #pragma unroll
                 for (int t = 0; t < 3; ++t) {
@@ -667,14 +744,10 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
         if (lane == 0) mbar_arrive(bars.p_full(w));
         if (u.flags & (kLast | kLastBut1)) {
             // the group's last unit of the item
-            float sum[HP];
-#pragma unroll
-            for (int h = 0; h < HP; ++h) {
-                sum[h] = l[h];
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], off);
-                if (lane == 0) red[64 + warp * 16 + h] = sum[h];
+            const float mine = warp_sums<HP>(l, lane);
+            if (lane < HP) {
+                own[kOwnL + lane] = mine;
+                own[kOwnRl + lane] = own[kOwnR + lane];
             }
             ok = ok && mbar_wait_warp<false>(bars.pv_done(w), turn.phase, wc);
             tc_fence_after();
@@ -684,56 +757,76 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
             bar_group(w);
             float x[HP];
 #pragma unroll
-            for (int h = 0; h < HP; ++h) {
-                sum[h] = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sum[h] += red[64 + k * 16 + h];
+            for (int h = 0; h < HP; ++h)
                 x[h] = 0.0078125f * fmaf(fmaf(__uint_as_float(o[2 * HP + h]), 0.0625f,
                                               __uint_as_float(o[HP + h])),
                                          0.0625f, __uint_as_float(o[h]));
-            }
+            // m, r and the sum of head hl over the group
+            float mh = own[kOwnM + hl], rh = kLowest, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rh = fmaxf(rh, group[k * kOwnSize + kOwnRl + hl]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                sum += group[k * kOwnSize + kOwnL + hl] *
+                       exp2_fast(group[k * kOwnSize + kOwnRl + hl] - rh);
             if (u.flags & kLastBut1) {  // the other group has the item's last
                 ok = ok && mbar_wait_warp<false>(bars.join_free(), joins.phase ^ 1u, wc);
                 if (ok) {
 #pragma unroll
-                    for (int h = 0; h < HP; ++h) {
-                        join[h * 130 + r] = x[h];
-                        if (r == 0) {
-                            join[h * 130 + 128] = m[h];
-                            join[h * 130 + 129] = sum[h];
-                        }
-                    }
+                    for (int h = 0; h < HP; ++h) join[h * 128 + r] = x[h];
+                    if (r < HP)
+                        *reinterpret_cast<float4 *>(join_stat + r * 4) = make_float4(mh, rh, sum, 0.f);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.join_full());
                 joins.next();
             } else {
+                float f[HP];
                 if (!(u.flags & kFirst)) {
                     ok = ok && mbar_wait_warp<false>(bars.join_full(), joins.phase, wc);
-#pragma unroll
-                    for (int h = 0; h < HP; ++h) {
-                        const float m1 = join[h * 130 + 128], mn = fmaxf(m[h], m1);
-                        const float f0 = m[h] == -INFINITY ? 0.f : exp2_fast(m[h] - mn);
-                        const float f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - mn);
-                        x[h] = x[h] * f0 + join[h * 130 + r] * f1;
-                        sum[h] = sum[h] * f0 + join[h * 130 + 129] * f1;
-                        m[h] = mn;
+                    const float4 o1 = *reinterpret_cast<const float4 *>(join_stat + hl * 4);
+                    const float mn = fmaxf(mh, o1.x), rn = fmaxf(rh, o1.y);
+                    if (lane < HP) {
+                        own[kOwnF + lane] = exp2_fast(mh - mn);
+                        own[kOwnFl + lane] = exp2_fast(o1.x - mn);
                     }
+                    sum = sum * exp2_fast(rh - rn) + o1.z * exp2_fast(o1.y - rn);
+                    mh = mn;
+                    rh = rn;
+                    __syncwarp();
+                    read_own<HP>(own + kOwnF, f);
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) x[h] *= f[h];
+                    read_own<HP>(own + kOwnFl, f);
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) x[h] = fmaf(join[h * 128 + r], f[h], x[h]);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bars.join_free());
                     joins.next();
                 }
+                if (u.flags & kWhole) {
+                    if (lane < HP) {
+                        const float half = half_factor(mh, rh);
+                        own[kOwnF + lane] = sum > 0.f || sum != sum ? half / sum : 0.f;
+                        own[kOwnFl + lane] = half;
+                    }
+                    __syncwarp();
+                    read_own<HP>(own + kOwnF, f);
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) x[h] *= f[h];
+                    read_own<HP>(own + kOwnFl, f);
+                }
 #pragma unroll
                 for (int h = 0; h < HP; ++h) {
                     if (h >= u.heads || !ok) break;
-                    if (u.flags & kWhole) {
+                    if (u.flags & kWhole)
                         p.out[(int64_t)u.b * p.out_stride + (int64_t)(u.head0 + h) * 128 + r] =
-                            __float2bfloat16(sum[h] > 0.f || sum[h] != sum[h] ? x[h] / sum[h] : 0.f);
-                    } else {
+                            __float2bfloat16(x[h] * f[h]);
+                    else
                         p.part_o[(int64_t)(u.slot + h) * 128 + r] = x[h];
-                        if (r == 0) p.part_ml[u.slot + h] = make_float2(m[h], sum[h]);
-                    }
                 }
+                if (!(u.flags & kWhole) && ok && r < u.heads)
+                    p.part_ml[u.slot + r] = make_float4(mh, rh, sum, 0.f);
             }
         }
         buf.next(2);
