@@ -308,6 +308,11 @@ wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t
  *            contents ignored; not shared by calls that overlap on the GPU.
  * The cache's rows are split over the whole GPU by their number, so the result
  * of a sequence depends on the other sequences' lengths in its last bits.
+ * Scores and sums in fp32.  The weights are rounded for the product: to bf16 over a bf16
+ * cache (2^-8 relative); over an E4M3 cache a weight times its value row's scale to
+ * 2^-11, or to 2^-25 of the sequence's largest such product, where that is more: value
+ * rows of scales 2^20 and more below those of the rows that count most lose bits.  Rows of
+ * zeros take no part in that, if their scale is 1 (as wanvae_kv_cache_append writes them).
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA. */
 size_t wanvae_paged_attention_workspace_size(int64_t n_heads, int64_t n_kv_heads,
                                              int64_t head_dim);

@@ -69,3 +69,39 @@ def test_paged_value_scales_beyond_fp32(cuda_lib, D, group, order):
             at += n
     cache, table, _, _ = fill(cuda_lib, lens, 32, 1, D, E4M3, seed=D + group, edit=edit)
     attended(cuda_lib, cache, table, lens, normal(gen(2), 2, group, D), group, scale, order)
+
+
+@pytest.mark.parametrize("D,group", HEADS)
+@pytest.mark.parametrize("size", [1e-4, 1e-6, 1e-20])
+def test_paged_value_rows_of_zeros(cuda_lib, D, group, size):
+    """Rows of zeros (scale 1 by the cache's definition) among rows of small values: they
+    add nothing to the output, and take no bits from the weights of the rows that do."""
+    lens, scale = [1500, 70, 256], D ** -0.5
+
+    def edit(k, v):
+        v *= size
+        v[::7] = 0
+        v[1500 + 3:1500 + 60] = 0
+        v[-1] = 0
+    cache, table, _, _ = fill(cuda_lib, lens, 16, 1, D, E4M3, seed=group, edit=edit)
+    attended(cuda_lib, cache, table, lens, normal(gen(3), 3, group, D), group, scale, size)
+
+
+@pytest.mark.parametrize("D,group", HEADS)
+def test_paged_value_row_of_zeros_takes_the_weight(cuda_lib, D, group):
+    """The row with by far the largest score has a value of zeros (a sink): the output is
+    small, and as exact as without it.  Rows of zeros and nothing else give zeros."""
+    n, scale = 1100, D ** -0.5
+    q = normal(gen(4), 2, group, D)
+    q[:, :, 0] = 4.0
+
+    def edit(k, v):
+        k[:, :, 0] = 0
+        for at in (0, 300, 301, 1099):  # scores of about 16 and 20 above the rest
+            k[at] = 0
+            k[at, :, 0] = 4 * scale ** -1 if at else 5 * scale ** -1
+            v[at] = 0
+        v[n:] = 0
+    cache, table, _, _ = fill(cuda_lib, [n, 300], 32, 1, D, E4M3, seed=group, edit=edit)
+    got = attended(cuda_lib, cache, table, [n, 300], q, group, scale)
+    assert torch.all(got[1] == 0)

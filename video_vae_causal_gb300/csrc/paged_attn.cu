@@ -31,11 +31,14 @@
 // 8-bit elements become fp16, exactly, on their way into the MMA (mma.sync of e4m3 operands
 // has no rate of its own here).  A query is scaled by a power of two that brings its
 // largest element to exponent 14, where bf16's 8 bits stay whole down to 2^-31 of it
-// and below that round to within 2^-39 of it; weights round once to fp16 (2^-12
-// relative).  A key row's scale multiplies its score; a value row's scale 2^e joins the
+// and below that round to within 2^-39 of it; weights round once to fp16.  A key row's scale multiplies its score; a value row's scale 2^e joins the
 // exponent of its weight, w_j = 2^(s_j + e_j - m) with m the running maximum of s_j + e_j,
 // so that weights stay in fp16's upper range whatever the scales are, while the sum takes
-// 2^(s_j - r) in fp32, r the running maximum of the scores alone (see paged_attn.cuh).
+// 2^(s_j - r) in fp32, r the running maximum of the scores alone (see paged_attn.cuh).  A
+// weight is off by 2^-11 of itself or, where that is more, by 2^-25 of the largest 2^(s + e);
+// rows of zeros (scale 1) do not count there.  They are looked for where m would move, which
+// is seldom: rows of e = 0 alone (any rows: 1.6 us more of 18, for 28803 rows of one kv head
+// over as many CTAs).
 //
 // What bounds it: HBM for 16-bit rows (64 sequences of 17 to 8192 rows, 8 kv heads of 4 query
 // heads of 128: 169 us, 6.1 TB/s, 0.90 of the measured copy rate; of 64: 89 us, 5.7 TB/s),
@@ -58,6 +61,7 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kJoinThreads = 128;
+constexpr float kLag = 4.f;  // how far a score may pass m before m moves
 // Keys of an item (a sequence and a block of heads), as far as the page table reaches, up
 // to which a CTA takes an item whole and no join follows; twice this where a quarter of
 // the CTAs have one, four times where all have.  Shared / apart, in us, tables of 16-row
@@ -314,6 +318,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                 for (int k = 0; k < 4; ++k) o[i][s][k] = 0.f;
         }
 
+        float least_e = INFINITY;
         for (int n = 0; n < units; ++n) {
             __syncwarp();  // the turn before this one is read: its place is free
             copy();
@@ -380,9 +385,19 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                     }
             }
             uint32_t pb[NH][NG][2];
+            // (least_e: see paged_attn.cuh)
+            bool low = false;
+            if (Q8) {
+                float x = INFINITY;
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x = min3(x, ve[i][j][0], ve[i][j][1]);
+                low = x < least_e;
+            }
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                float s[NG][2][2], mx = -INFINITY;
+                float s[NG][2][2], mx;
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -400,16 +415,67 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                                 if (8 * j + S::row_of(2 * t + c) >= ((rows >> (8 * i)) & 0xff))
                                     s[i][j][c] = -INFINITY;
                 }
+                float sv[NG][2][2];  // with the value rows' exponents
+                auto largest = [&]() {
+                    mx = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < NG; ++i)
+                    for (int i = 0; i < NG; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        mx = max3(mx, s[i][j][0] + ve[i][j][0], s[i][j][1] + ve[i][j][1]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        for (int j = 0; j < 2; ++j) {
+                            sv[i][j][0] = s[i][j][0] + ve[i][j][0];
+                            sv[i][j][1] = s[i][j][1] + ve[i][j][1];
+                            mx = max3(mx, sv[i][j][0], sv[i][j][1]);
+                        }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                };
+                largest();
                 // the maximum moves only by more than 2^4: weights stay below 16,
                 // their sums below fp16's products' fp32 range, and O is seldom rescaled
-                if (__any_sync(0xffffffffu, mx > m[h] + 4.f)) {
+                if (__any_sync(0xffffffffu, mx > m[h] + kLag || low)) {
+                    if (Q8) {
+                        // A value row of zeros (scale 1: e = 0) has no part in the maximum:
+                        // it would take the bits of the weights that count.  The eight
+                        // lanes of a t look at a row together.
+                        bool unsure = false;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                unsure |= ve[i][j][0] == 0.f || ve[i][j][1] == 0.f;
+                        if (__any_sync(0xffffffffu, unsure)) {
+#pragma unroll
+                            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c) {
+                                        const int row = 8 * j + S::row_of(2 * t + c);
+                                        const uint2 *a = reinterpret_cast<const uint2 *>(
+                                            src + i * 2 * S::kHalf + S::kHalf +
+                                            S::piece(row, S::VB == 16 ? g : g >> 1));
+                                        uint2 x = a[S::VB == 16 ? 0 : g & 1];
+                                        if (S::VB == 16) {
+                                            const uint2 y = a[1];
+                                            x.x |= y.x;
+                                            x.y |= y.y;
+                                        }
+                                        const bool some = ((x.x | x.y) & 0x7f7f7f7fu) != 0u;
+                                        const unsigned any = __ballot_sync(0xffffffffu, some);
+                                        if (!(any & (0x11111111u << t)) && ve[i][j][c] == 0.f) {
+                                            ve[i][j][c] = -INFINITY;
+                                            low = true;  // (for the other 8 heads)
+                                        }
+                                    }
+                            largest();
+                        }
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) top = max3(top, s[i][j][0], s[i][j][1]);
+                        raise_sum(top, r[h], l[h]);
+                    }
                     const float mn = fmaxf(m[h], mx);
                     const float f = exp2_fast(m[h] - mn);
                     m[h] = mn;
@@ -423,14 +489,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                         o[h][k][2] *= f0;
                         o[h][k][3] *= f1;
                     }
-                }
-                if (Q8) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < NG; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) top = max3(top, s[i][j][0], s[i][j][1]);
-                    raise_sum(top, kSumLag, r[h], l[h]);
+                    if (Q8)
+                        least_e = fmaxf(m[0] - r[0], m[NH - 1] - r[NH - 1]) - (kSumLag - kLag);
                 }
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
@@ -441,7 +501,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                         for (int c = 0; c < 2; ++c) {
                             const float e = exp2_fast(s[i][j][c] - (Q8 ? r[h] : m[h]));
                             l[h] += e;
-                            w[j][c] = Q8 ? exp2_fast(s[i][j][c] + (ve[i][j][c] - m[h])) : e;
+                            w[j][c] = Q8 ? exp2_fast(sv[i][j][c] - m[h]) : e;
                         }
                     pb[h][i][0] = pack16<Q8>(w[0][0], w[0][1]);
                     pb[h][i][1] = pack16<Q8>(w[1][0], w[1][1]);
@@ -554,32 +614,45 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
         }
         __syncthreads();
         const int slot = 2 * blockIdx.x + (first ? 0 : 1);
-        for (int e = threadIdx.x; e < heads * D; e += kThreads) {
-            const int h = e / D, d = e % D;
-            const int i = h >> 3, hr = h & 7;
+        if (threadIdx.x < heads) {
+            // a thread for each head: the warps' factors in place of their m, and with the
+            // first the head's sum and half_factor
+            const int h = threadIdx.x, i = h >> 3, hr = h & 7;
             float4 mw[kWarps];
-            float top = kLowest, rtop = kLowest;
+            float top = kLowest, rtop = kLowest, sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 mw[w] = ml[(w * NH + i) * 8 + hr];
                 top = fmaxf(top, mw[w].x);
                 if (Q8) rtop = fmaxf(rtop, mw[w].y);
             }
-            float sum = 0.f, acc = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float f = exp2_fast(mw[w].x - top);
                 sum += (Q8 ? exp2_fast(mw[w].y - rtop) : f) * mw[w].z;
-                acc += f * reinterpret_cast<const float *>(
-                               smem + (w * S::kStages + last) * S::kTurn)
-                               [i * S::kJoinHeads + d * 8 + (d >> 4) * S::kPad + hr];
+                ml[(w * NH + i) * 8 + hr].x = f;
             }
+            ml[i * 8 + hr].y = Q8 ? half_factor(top, rtop) : 1.f;
+            ml[i * 8 + hr].z = sum;
+            if (!whole) p.part_ml[slot * (8 * NH) + h] = make_float4(top, rtop, sum, 0.f);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < heads * D; e += kThreads) {
+            const int h = e / D, d = e % D;
+            const int i = h >> 3, hr = h & 7;
+            float acc = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                acc += ml[(w * NH + i) * 8 + hr].x *
+                       reinterpret_cast<const float *>(
+                           smem + (w * S::kStages + last) * S::kTurn)
+                           [i * S::kJoinHeads + d * 8 + (d >> 4) * S::kPad + hr];
+            const float4 all = ml[i * 8 + hr];
             if (whole) {
                 p.out[(int64_t)at.b * p.out_stride + (int64_t)(h0 + h) * D + d] =
-                    __float2bfloat16(output_of<Q8>(acc, sum, top, rtop));
+                    __float2bfloat16(output_of<Q8>(acc, all.z, all.y));
             } else {
                 p.part_o[((int64_t)slot * (8 * NH) + h) * D + d] = acc;
-                if (d == 0) p.part_ml[slot * (8 * NH) + h] = make_float4(top, rtop, sum, 0.f);
             }
         }
         fence_proxy_async_smem();  // the buffers' next writer is the TMA
@@ -690,7 +763,7 @@ paged_join_kernel(const PagedArgs p, int block_heads) {
             a += acc_w[w][tid];
             sum += warp_l[w];
         }
-        out[tid] = __float2bfloat16(output_of<Q8>(a, sum, top, rtop));
+        out[tid] = __float2bfloat16(output_of<Q8>(a, sum, Q8 ? half_factor(top, rtop) : 1.f));
     }
 }
 

@@ -167,19 +167,18 @@ constexpr float kSumLag = 60.f;  // (2^31 rows of 2^60 stay in fp32's range)
 // no scales, and one reference.)
 __device__ __forceinline__ float half_factor(float m, float r) { return exp2_fast(0.5f * (m - r)); }
 template <bool Q8>
-__device__ __forceinline__ float output_of(float acc, float sum, float m, float r) {
+__device__ __forceinline__ float output_of(float acc, float sum, float half) {
     const float o = sum > 0.f || sum != sum ? acc / sum : 0.f;
-    if (!Q8) return o;
-    const float f = half_factor(m, r);
-    return o * f * f;
+    return Q8 ? o * half * half : o;
 }
 
-// Moves r, and the sum l with it, where `top` lies more than `lag` above it.
-__device__ __forceinline__ void raise_sum(float top, float lag, float &r, float &l) {
-    if (top > r + lag) {
-        l *= exp2_fast(r - top);
-        r = top;
-    }
+// That no s lies more than kSumLag above r is seen from the value rows' exponents alone: s + e
+// is at most m and a lag of m's, so that e >= least_e = m - r - (kSumLag - that lag) will do,
+// one comparison a row for all heads.  Where it does not hold, or m moves, r moves up:
+__device__ __forceinline__ void raise_sum(float top, float &r, float &l) {
+    const float rn = fmaxf(r, top);
+    l *= exp2_fast(r - rn);
+    r = rn;
 }
 
 // The CTAs of a launch: as many as there can be units, at most `most`.
