@@ -253,7 +253,8 @@ wanvae_status wanvae_packed_attention(const void *q, int64_t q_stride, const voi
  * of the sequence lies in slot p % page_size of its page p / page_size.
  *   k, v  : [n_pages][n_kv_heads][page_size][head_dim], of type dt
  *   dt    : WANVAE_BF16, or WANVAE_E4M3: a row (one token, one head) holds
- *           e4m3 elements q and one E8M0 scale, x[d] = q[d] * 2^(code - 127)
+ *           e4m3 elements q and one E8M0 scale, x[d] = q[d] * 2^(code - 127); what
+ *           passes bf16's largest value counts as that value where values are read
  *   k_exp, v_exp : [n_pages][n_kv_heads][page_size] scale codes (E4M3 only), 27
  *           to 247 (2^-100 to 2^120) in rows that attention reads
  *   page_size : 16, 32, 64, .. 1024.  head_dim : 64 or 128. */

@@ -105,3 +105,28 @@ def test_paged_value_row_of_zeros_takes_the_weight(cuda_lib, D, group):
     cache, table, _, _ = fill(cuda_lib, [n, 300], 32, 1, D, E4M3, seed=group, edit=edit)
     got = attended(cuda_lib, cache, table, [n, 300], q, group, scale)
     assert torch.all(got[1] == 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_cache_largest_values_come_back_finite(cuda_lib, D):
+    """Magnitudes above 1.9375 * 2^127 round to 256 * 2^120 = 2^128, half a step beyond bf16's
+    largest value: read back and attended to, they are that value, not an infinity."""
+    n = 40
+    x = torch.full((n, 1, D), BF16_MAX, dtype=torch.bfloat16, device=DEV)
+    x[:, :, 1::2] = -BF16_MAX
+    x[1, 0, 2], x[2, 0, 3] = 0.0, 1.875 * 2.0 ** 127
+    x[3, 0, 4] = math.nan
+    k = torch.zeros_like(x)
+    cache = cuda_lib.make_kv_cache(3, 16, 1, D)
+    table = ints([[2, 0, 1]])
+    cuda_lib.kv_cache_append(cache, k, x, ints([n]), table, ints([0, n]))
+    _, v = cuda_lib.kv_cache_gather(cache, table, ints([0, n]), total=n)
+    cuda_lib.sync_status()
+    want = rows_of(cache, table, 0, n)[1].clamp(-BF16_MAX, BF16_MAX)
+    assert torch.isfinite(want).sum() == want.numel() - 1
+    assert torch.equal(torch.isnan(v.double()), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(v.double()), torch.nan_to_num(want))
+    # rows 0 and 1 alone: no NaN among them
+    for group in (4, 8, 12):
+        attended(cuda_lib, cache, table, [2], normal(gen(5), 1, group, D), group, D ** -0.5)
+        attended(cuda_lib, cache, table, [1], normal(gen(5), 1, group, D), group, D ** -0.5)

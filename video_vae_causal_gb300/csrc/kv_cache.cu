@@ -9,8 +9,9 @@
 // step of e4m3 (2^-4 relative, above e4m3's subnormals).  e stays in
 // [-100, 120]: 2^120 * 448 covers every finite bf16 value, and rows below 2^-100
 // round on the grid of 2^-100 (so that attention can carry scales as
-// exponents without leaving fp32's range).  Infinities and NaN become e4m3's
-// NaN and do not count for the scale.
+// exponents without leaving fp32's range).  Magnitudes from 1.9375 * 2^127 on round to
+// 256 * 2^120 = 2^128, which reads back as the largest bf16 value.  Infinities and NaN become
+// e4m3's NaN and do not count for the scale.
 //
 // Rows lie [page][head][slot][D]: the rows of one head and page are
 // contiguous, which is how attention over the cache reads them.  Both passes
@@ -107,7 +108,15 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &v, int &e) {
     return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
-// 8 e4m3 values of a row -> bf16 (exact for scales that leave bf16's range alone).
+// nact_pack, with what passes the largest value as that value (a NaN stays one; tested).
+__device__ __forceinline__ uint32_t pack_finite(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 8 e4m3 values of a row -> bf16 (exact for scales that leave bf16's range alone; what
+// passes its largest value is that value, as nothing that is stored is infinite).
 __device__ __forceinline__ uint4 dequantise8(const uint2 &q, uint32_t code) {
     const float s = e8m0_value(code);
     const uint32_t w[2] = {q.x, q.y};
@@ -116,7 +125,7 @@ __device__ __forceinline__ uint4 dequantise8(const uint2 &q, uint32_t code) {
     for (int i = 0; i < 4; ++i) {
         const uint32_t h = e4m3x2_to_f16x2(w[i >> 1] >> (16 * (i & 1)));
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        o[i] = nact_pack(f.x * s, f.y * s);
+        o[i] = pack_finite(f.x * s, f.y * s);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }

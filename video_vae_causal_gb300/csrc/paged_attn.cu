@@ -650,7 +650,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
             const float4 all = ml[i * 8 + hr];
             if (whole) {
                 p.out[(int64_t)at.b * p.out_stride + (int64_t)(h0 + h) * D + d] =
-                    __float2bfloat16(output_of<Q8>(acc, all.z, all.y));
+                    to_output<Q8>(output_of<Q8>(acc, all.z, all.y));
             } else {
                 p.part_o[((int64_t)slot * (8 * NH) + h) * D + d] = acc;
             }
@@ -763,7 +763,8 @@ paged_join_kernel(const PagedArgs p, int block_heads) {
             a += acc_w[w][tid];
             sum += warp_l[w];
         }
-        out[tid] = __float2bfloat16(output_of<Q8>(a, sum, Q8 ? half_factor(top, rtop) : 1.f));
+        out[tid] =
+            to_output<Q8>(output_of<Q8>(a, sum, Q8 ? half_factor(top, rtop) : 1.f));
     }
 }
 

@@ -172,6 +172,15 @@ __device__ __forceinline__ float output_of(float acc, float sum, float half) {
     return Q8 ? o * half * half : o;
 }
 
+// An output as bf16.  What 8-bit rows hold is finite or NaN, so a sum that passes bf16's
+// largest value is that value (rows near it round to 2^128; read back they saturate too).
+template <bool Q8>
+__device__ __forceinline__ __nv_bfloat16 to_output(float v) {
+    const float most = __uint_as_float(0x7f7f0000u);
+    if (Q8 && v == v) v = fminf(fmaxf(v, -most), most);
+    return __float2bfloat16(v);
+}
+
 // That no s lies more than kSumLag above r is seen from the value rows' exponents alone: s + e
 // is at most m and a lag of m's, so that e >= least_e = m - r - (kSumLag - that lag) will do,
 // one comparison a row for all heads.  Where it does not hold, or m moves, r moves up:

@@ -846,7 +846,7 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
                     if (h >= u.heads || !ok) break;
                     if (u.flags & kWhole)
                         p.out[(int64_t)u.b * p.out_stride + (int64_t)(u.head0 + h) * 128 + r] =
-                            __float2bfloat16(x[h] * f[h]);
+                            to_output<true>(x[h] * f[h]);
                     else
                         p.part_o[(int64_t)(u.slot + h) * 128 + r] = x[h];
                 }
