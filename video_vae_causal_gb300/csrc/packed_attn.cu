@@ -140,8 +140,10 @@ struct Bars {
 };
 
 // Tile pair `x` of the launch, counting the pairs of every sequence in order;
-// whole warp.  nq = 0: no such pair.
-__device__ Tile find_tile(const PackedArgs &p, int x) {
+// whole warp.  nq = 0: no such pair.  `tell`: report offsets that leave the tensors (the
+// launch's last pair does: one more than sequences in order can have, it comes by all of them
+// up to the first that is out of order).
+__device__ Tile find_tile(const PackedArgs &p, int x, bool tell) {
     const int lane = threadIdx.x & 31;
     Tile r = {0, 0, 0, 0, 0};
     int before = 0;
@@ -156,7 +158,7 @@ __device__ Tile find_tile(const PackedArgs &p, int x) {
             // offsets that leave the tensors count for nothing
             const bool ok = qa >= 0 && qb >= qa && qb <= p.total_q && ka >= 0 && kb >= ka &&
                             kb <= p.total_k;
-            if (!ok && x == 0) atomicOr(p.err, kDevErrAlign);
+            if (!ok && tell) atomicOr(p.err, kDevErrAlign);
             tiles = ok ? (qb - qa + 2 * p.nt - 1) / (2 * p.nt) : 0;
         }
         int incl = tiles;
@@ -601,7 +603,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant
     const WaitCtl wc{p.wait_ns, p.err, abort_flag, 0u};
     griddep_wait();
     const int kvh = blockIdx.x % p.Hkv;
-    const Tile tl = find_tile(p, blockIdx.x / p.Hkv);
+    const Tile tl = find_tile(p, blockIdx.x / p.Hkv,
+                              blockIdx.x == gridDim.x - 1);
     const int keys[2] = {keys_of(p, tl, 0), keys_of(p, tl, 1)};
     const int n0 = turns_of<D>(keys[0]), n1 = turns_of<D>(keys[1]);
     const int keys_cta = max(keys[0], keys[1]), blocks = (max(n0, n1) + L::kPer - 1) / L::kPer;
