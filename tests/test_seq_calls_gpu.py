@@ -39,3 +39,52 @@ def test_packed_bad_offsets_are_reported_wherever_they_are(cuda_lib, lens, bad, 
                                     causal_mask(n, n), 0.125)
                 close(out[at:at + n, h], o, a, f"sequence {s}")
         at += n
+
+
+def pool_of(t):
+    """The stream whose memory a tensor lies in."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's")
+
+
+@pytest.mark.parametrize("what", ["packed", "gather", "paged", "norm"])
+def test_results_lie_in_the_memory_of_the_call_s_stream(cuda_lib, what, monkeypatch):
+    """With stream= and no outputs given, what the call allocates belongs to that stream: a
+    block out of the current stream's memory may still be in use there.  (The streams
+    are idle here: nothing overlaps.)"""
+    g = gen(1)
+    x = normal(g, 48, 2, 64)
+    cache = cuda_lib.make_kv_cache(3, 16, 2, 64)
+    table, lens, cu = ints([[0, 1, 2]]), ints([48]), ints([0, 48])
+    cuda_lib.kv_cache_append(cache, x, x, lens, table, cu)
+    made = []
+    real = cuda_lib.make_paged_attention_workspace
+
+    def workspace(*args):
+        made.append(real(*args))
+        return made[-1]
+    monkeypatch.setattr(cuda_lib, "make_paged_attention_workspace", workspace)
+
+    def call(stream):
+        if what == "packed":
+            return [cuda_lib.packed_attention(x, x, x, cu, stream=stream)]
+        if what == "gather":
+            return list(cuda_lib.kv_cache_gather(cache, table, cu, total=48, stream=stream))
+        if what == "paged":
+            return [cuda_lib.paged_attention(x[:1], cache, lens, table, stream=stream)]
+        ones = torch.ones(64, device=DEV)
+        return list(cuda_lib.gated_residual_norm(x, x, ones, None, ones, stream=stream))
+    torch.cuda.synchronize()
+    want = call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = call(side)
+    side.synchronize()
+    cuda_lib.sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    for t in got + made[1:]:
+        assert pool_of(t) == side.cuda_stream
+    assert pool_of(want[0]) != side.cuda_stream
+    assert len(made) == (2 if what == "paged" else 0)

@@ -440,10 +440,21 @@ def _ints(where, t, *shape):
         raise WanvaeError(ERR_INVALID_ARG, where)
 
 
-def _ours(t, stream):
-    """A tensor allocated here for work on a stream that may not be current."""
+def _on_stream(stream, make, *args, **kw):
+    """make(..) out of the memory of the stream that the call works on: a block of the
+    current stream's may still be in use there."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _result(stream, make, *args, **kw):
+    """_on_stream for what is returned: its memory is not reused before the current stream
+    is done with it."""
+    t = _on_stream(stream, make, *args, **kw)
     if stream is not None:
-        t.record_stream(stream)
+        t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -454,9 +465,9 @@ def packed_attention(q, k, v, cu_q, cu_k=None, out=None, causal=True, scale=None
     given); causal: the last query of a sequence sees all of its keys.  Rows of
     `out` behind the last sequence are left as they were."""
     where = "wanvae_packed_attention"
-    if out is None:
-        out = _ours(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
     dev = _on_device(where, q, k, v, cu_q, cu_k, out)
+    if out is None:
+        out = _result(stream, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
     n = cu_q.numel() - 1
     _ints(where, cu_q, n + 1)
     if cu_k is None:
@@ -543,11 +554,11 @@ def kv_cache_gather(cache, page_table, cu, k=None, v=None, total=None, stream=No
     cu[s] .. cu[s + 1] - 1 of k and v [total, Hkv, D] bf16 (cu int32 [n + 1],
     device).  Without k and v, `total` rows are allocated."""
     where = "wanvae_kv_cache_gather"
+    dev = _on_device(where, page_table, cu, k, v)
     if k is None or v is None:
         _fit(where, k is None and v is None and total is not None)
-        k, v = (_ours(torch.empty((total, cache.heads, cache.head_dim), dtype=torch.bfloat16,
-                                  device=page_table.device), stream) for _ in range(2))
-    dev = _on_device(where, k, v, cu, page_table)
+        k, v = (_result(stream, torch.empty, (total, cache.heads, cache.head_dim),
+                        dtype=torch.bfloat16, device=page_table.device) for _ in range(2))
     ks, vs = _heads(where, k), _heads(where, v)
     T = k.shape[0]
     shape = (T, cache.heads, cache.head_dim)
@@ -579,11 +590,11 @@ def paged_attention(q, cache, lens, page_table, out=None, workspace=None, scale=
     first lens[s] positions of the cache (lens int32 [n], page_table int32
     [n, max_pages], device); zeros where lens[s] is 0."""
     where = "wanvae_paged_attention"
-    if out is None:
-        out = _ours(torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), stream)
-    if workspace is None:
-        workspace = _ours(make_paged_attention_workspace(q, cache), stream)
     dev = _on_device(where, q, lens, page_table, out, workspace)
+    if out is None:
+        out = _result(stream, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
+    if workspace is None:
+        workspace = _on_stream(stream, make_paged_attention_workspace, q, cache)
     qs, os_ = _heads(where, q), _heads(where, out)
     shape = q.shape
     n, Hq, D = shape
@@ -608,11 +619,11 @@ def gated_residual_norm(x, f, gamma_post=None, gate=None, gamma_pre=None, tokens
     or fp32, contiguous).  gate fp32 [G, C]: token i has row i // tokens_per_gate.
     Returns (y, n); n is None without gamma_pre."""
     where = "wanvae_gated_residual_norm"
-    if y is None:
-        y = _ours(torch.empty_like(x), stream)
-    if n is None and gamma_pre is not None:
-        n = _ours(torch.empty_like(x), stream)
     dev = _on_device(where, x, f, gamma_post, gate, gamma_pre, y, n)
+    if y is None:
+        y = _result(stream, torch.empty_like, x)
+    if n is None and gamma_pre is not None:
+        n = _result(stream, torch.empty_like, x)
     shape, dtype = x.shape, x.dtype
     _fit(where, (dtype == torch.bfloat16 or dtype == torch.float32) and x.is_contiguous())
     for t in (f, y, n):
