@@ -27,6 +27,9 @@ size_t span(int64_t n, int64_t stride, int64_t width) {
     return n < 1 ? 0 : ((size_t)(n - 1) * stride + width) * 2;
 }
 
+// Bytes of n int32 values.
+size_t ints(int64_t n) { return (size_t)n * 4; }
+
 // Whether rows of two tensors collide: n tokens of `width` elements each, which may
 // lie side by side in one buffer where their strides are equal.
 bool rows_collide(const void *a, int64_t a_stride, const void *b, int64_t b_stride, int64_t n,
@@ -122,7 +125,8 @@ wanvae_status wanvae_packed_attention(const void *q, int64_t q_stride, const voi
     const size_t ob = span(total_q, out_stride, wq);
     if (overlap(out, ob, q, span(total_q, q_stride, wq)) ||
         overlap(out, ob, k, span(total_k, k_stride, wk)) ||
-        overlap(out, ob, v, span(total_k, v_stride, wk)))
+        overlap(out, ob, v, span(total_k, v_stride, wk)) ||
+        overlap(out, ob, cu_q, ints(n_seq + 1)) || overlap(out, ob, cu_k, ints(n_seq + 1)))
         return WANVAE_ERR_INVALID_ARG;
     PackedAttnSpec s;
     s.q = q;
@@ -167,7 +171,9 @@ wanvae_status wanvae_kv_cache_append(const wanvae_kv_cache *cache, const void *k
     if (misaligned(k) || misaligned(v) || misaligned(lens, 4) || misaligned(page_table, 4) ||
         misaligned(cu_new, 4))
         return WANVAE_ERR_MISALIGNED;
-    if (touches(s, k, span(total, k_stride, w)) || touches(s, v, span(total, v_stride, w)))
+    if (touches(s, k, span(total, k_stride, w)) || touches(s, v, span(total, v_stride, w)) ||
+        touches(s, lens, ints(n_seq)) || touches(s, page_table, ints(n_seq * max_pages)) ||
+        (cu_new && touches(s, cu_new, ints(n_seq + 1))))
         return WANVAE_ERR_INVALID_ARG;
     LaunchCtx ctx;
     if (!make_launch_ctx(ctx, stream)) return WANVAE_ERR_CUDA;
@@ -191,8 +197,11 @@ wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t
     if (!stride_ok(k_stride, w) || !stride_ok(v_stride, w)) return WANVAE_ERR_INVALID_ARG;
     if (misaligned(k) || misaligned(v) || misaligned(cu, 4) || misaligned(page_table, 4))
         return WANVAE_ERR_MISALIGNED;
-    if (rows_collide(k, k_stride, v, v_stride, total, w) ||
-        touches(s, k, span(total, k_stride, w)) || touches(s, v, span(total, v_stride, w)))
+    const size_t kb = span(total, k_stride, w), vb = span(total, v_stride, w);
+    const size_t cb = ints(n_seq + 1), tb = ints(n_seq * max_pages);
+    if (rows_collide(k, k_stride, v, v_stride, total, w) || touches(s, k, kb) ||
+        touches(s, v, vb) || overlap(k, kb, cu, cb) || overlap(v, vb, cu, cb) ||
+        overlap(k, kb, page_table, tb) || overlap(v, vb, page_table, tb))
         return WANVAE_ERR_INVALID_ARG;
     LaunchCtx ctx;
     if (!make_launch_ctx(ctx, stream)) return WANVAE_ERR_CUDA;
@@ -237,8 +246,11 @@ wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
     if (!workspace || ws_bytes < need) return WANVAE_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return WANVAE_ERR_MISALIGNED;
     const size_t qb = span(n_seq, q_stride, w), ob = span(n_seq, out_stride, w);
+    const size_t lb = ints(n_seq), tb = ints(n_seq * max_pages);
     if (overlap(q, qb, out, ob) || touches(s, out, ob) || touches(s, workspace, need) ||
-        overlap(workspace, need, q, qb) || overlap(workspace, need, out, ob))
+        overlap(workspace, need, q, qb) || overlap(workspace, need, out, ob) ||
+        overlap(out, ob, lens, lb) || overlap(out, ob, page_table, tb) ||
+        overlap(workspace, need, lens, lb) || overlap(workspace, need, page_table, tb))
         return WANVAE_ERR_INVALID_ARG;
     LaunchCtx ctx;
     if (!make_launch_ctx(ctx, stream)) return WANVAE_ERR_CUDA;
