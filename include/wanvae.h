@@ -272,13 +272,13 @@ typedef struct {
  * has scale 1.
  *   k, v   : bf16 [total][n_kv_heads][head_dim], tokens k_stride / v_stride apart
  *   lens   : device int32 [n_seq], each sequence's length WITH its new tokens
- *   cu_new : device int32 [n_seq + 1]: sequence s's new tokens are rows
- *            cu_new[s] .. cu_new[s+1] - 1, its last positions; NULL: one new
- *            token for each sequence (total = n_seq)
+ *   cu_new : device int32 [n_seq + 1], from 0, not decreasing, at most total:
+ *            sequence s's new tokens are rows cu_new[s] .. cu_new[s+1] - 1, its last
+ *            positions; NULL: one new token for each sequence (total = n_seq)
  * No two tokens of a call may lie in the same slot (sequences may share pages that
  * the call does not write).  A token whose position or page lies outside the page
- * table or the cache is not written, and wanvae_sync_status reports
- * WANVAE_ERR_CUDA.
+ * table or the cache, or whose sequence ends behind total, is not written, and
+ * wanvae_sync_status reports WANVAE_ERR_CUDA.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_kv_cache_append(const wanvae_kv_cache *cache, const void *k,
                                      int64_t k_stride, const void *v, int64_t v_stride,
@@ -289,9 +289,10 @@ wanvae_status wanvae_kv_cache_append(const wanvae_kv_cache *cache, const void *k
 /* The cache read back, packed, for wanvae_packed_attention over new tokens:
  * positions 0 .. of sequence s to the rows cu[s] .. cu[s+1] - 1 of k and v
  * (bf16 [total][n_kv_heads][head_dim], tokens k_stride / v_stride apart; both
- * may lie side by side in rows of one buffer).  Rows behind the last sequence,
- * and rows whose page lies outside the page table or the cache (reported as for
- * wanvae_kv_cache_append), are left as they were.
+ * may lie side by side in rows of one buffer), cu as cu_new above.  Rows behind the
+ * last sequence, and rows whose page lies outside the page table or the cache or whose
+ * sequence ends behind total (reported as for wanvae_kv_cache_append), are left as they
+ * were.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t *page_table,
                                      int64_t max_pages, const int32_t *cu, int64_t n_seq,

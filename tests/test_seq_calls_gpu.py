@@ -88,3 +88,33 @@ def test_results_lie_in_the_memory_of_the_call_s_stream(cuda_lib, what, monkeypa
         assert pool_of(t) == side.cuda_stream
     assert pool_of(want[0]) != side.cuda_stream
     assert len(made) == (2 if what == "paged" else 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e4m3fn, torch.bfloat16])
+def test_cache_offsets_behind_the_rows_are_reported(cuda_lib, dtype):
+    """A sequence that ends behind the rows that are given is left out and reported, in
+    append and in gather; the others are not touched by that."""
+    g = gen(2)
+    k, v = normal(g, 50, 2, 64), normal(g, 50, 2, 64)
+    table, lens = ints([[0, 1], [2, 3], [4, 5]]), ints([20, 32, 10])
+    cu, broken = ints([0, 20, 40, 50]), ints([0, 20, 60, 70])
+    whole, cache = (cuda_lib.make_kv_cache(6, 16, 2, 64, dtype=dtype) for _ in range(2))
+    cuda_lib.kv_cache_append(whole, k, v, lens, table, cu)
+    cuda_lib.sync_status()
+    before = [t.view(torch.uint8).clone() for t in cache.tensors() if t is not None]
+    cuda_lib.kv_cache_append(cache, k, v, lens, table, broken)
+    with pytest.raises(cuda_lib.WanvaeError) as ei:
+        cuda_lib.sync_status()
+    assert ei.value.status == cuda_lib.ERR_CUDA
+    for a, b, c in zip((t for t in cache.tensors() if t is not None),
+                       (t for t in whole.tensors() if t is not None), before):
+        a, b = a.view(torch.uint8), b.view(torch.uint8)
+        assert torch.equal(a[:2], b[:2]) and torch.equal(a[2:], c[2:])
+    want_k, want_v = cuda_lib.kv_cache_gather(whole, table, cu, total=50)
+    cuda_lib.sync_status()
+    out_k, out_v = torch.full_like(want_k, 7.0), torch.full_like(want_v, 7.0)
+    cuda_lib.kv_cache_gather(whole, table, broken, k=out_k, v=out_v)
+    with pytest.raises(cuda_lib.WanvaeError):
+        cuda_lib.sync_status()
+    for got, want in ((out_k, want_k), (out_v, want_v)):
+        assert torch.equal(got[:20], want[:20]) and torch.all(got[20:] == 7.0)

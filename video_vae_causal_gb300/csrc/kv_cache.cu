@@ -178,7 +178,7 @@ kv_append_kernel(const CacheArgs c, const __nv_bfloat16 *__restrict__ k, int64_t
             len = __ldg(lens + seq);
         }
         if (t < first || t >= end) continue;  // a row behind the last sequence
-        const int64_t row0 = cache_row(c, seq, len - (end - t));
+        const int64_t row0 = end > total ? -1 : cache_row(c, seq, len - (end - t));
         if (row0 < 0) {
             if (lane == 0) atomicOr(c.err, kDevErrAlign);
             continue;
@@ -226,7 +226,7 @@ kv_gather_kernel(const CacheArgs c, const int32_t *__restrict__ cu, int n_seq, i
             end = __ldg(cu + seq + 1);
         }
         if (t < first || t >= end) continue;
-        const int64_t row0 = cache_row(c, seq, t - first);
+        const int64_t row0 = end > total ? -1 : cache_row(c, seq, t - first);
         if (row0 < 0) {
             if (lane == 0) atomicOr(c.err, kDevErrAlign);
             continue;
