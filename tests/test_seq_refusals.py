@@ -36,3 +36,11 @@ def test_gather_refuses_offsets_and_pages_in_its_outputs(lib, edit):  # noqa: F8
 def test_paged_attention_refuses_lengths_and_pages_in_what_it_writes(lib, edit):  # noqa: F811
     """2 sequences: lengths of 8 bytes, 2 x 2 pages."""
     assert decode(lib, **edit) == ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("stride", [0, 4, 132, 1000])
+def test_one_token_s_stride_means_nothing(stride):
+    """A single token out of a buffer whose rows would not do for several."""
+    buf = torch.zeros(4096, dtype=torch.bfloat16)
+    assert wanvae._heads("", buf.as_strided((1, 2, 64), (stride, 64, 1))) == 128
+    assert wanvae._heads("", buf.as_strided((2, 2, 64), (132, 64, 1))) == 132

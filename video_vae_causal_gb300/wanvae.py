@@ -432,7 +432,7 @@ def _heads(where, t):
     sn, sh, sd = t.stride()
     if (h > 1 and sh != d) or (d > 1 and sd != 1):
         raise WanvaeError(ERR_INVALID_ARG, where)
-    return sn if n > 1 else max(sn, h * d)
+    return sn if n > 1 else h * d  # (one token's stride means nothing)
 
 
 def _ints(where, t, *shape):
