@@ -44,3 +44,13 @@ def test_one_token_s_stride_means_nothing(stride):
     buf = torch.zeros(4096, dtype=torch.bfloat16)
     assert wanvae._heads("", buf.as_strided((1, 2, 64), (stride, 64, 1))) == 128
     assert wanvae._heads("", buf.as_strided((2, 2, 64), (132, 64, 1))) == 132
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The launch would fail there, and leave its error for the next one to find."""
+    class Stream:
+        cuda_stream, device_index = 7, 1
+    assert wanvae._raw_stream("", Stream, 1) == 7
+    with pytest.raises(wanvae.WanvaeError) as ei:
+        wanvae._raw_stream("", Stream, 0)
+    assert ei.value.status == ERR_INVALID_ARG

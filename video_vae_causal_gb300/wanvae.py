@@ -420,8 +420,11 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _raw_stream(stream, device):
-    return _current_raw_stream(device) if stream is None else stream.cuda_stream
+def _raw_stream(where, stream, device):
+    if stream is None:
+        return _current_raw_stream(device)
+    _fit(where, stream.device_index == device)
+    return stream.cuda_stream
 
 
 def _heads(where, t):
@@ -481,7 +484,7 @@ def packed_attention(q, k, v, cu_q, cu_k=None, out=None, causal=True, scale=None
     st = load().wanvae_packed_attention(
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, out.data_ptr(), os_,
         cu_q.data_ptr(), cu_k.data_ptr(), n, Tq, kshape[0], Hq, kshape[1], D,
-        D ** -0.5 if scale is None else scale, 1 if causal else 0, _raw_stream(stream, dev))
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, _raw_stream(where, stream, dev))
     _check(st, where)
     return out
 
@@ -545,7 +548,7 @@ def kv_cache_append(cache, k, v, lens, page_table, cu_new=None, stream=None):
         _ints(where, cu_new, n + 1)
     st = load().wanvae_kv_cache_append(cache.ref, k.data_ptr(), ks, v.data_ptr(), vs,
                                        lens.data_ptr(), page_table.data_ptr(), max_pages,
-                                       _raw(cu_new), n, T, _raw_stream(stream, dev))
+                                       _raw(cu_new), n, T, _raw_stream(where, stream, dev))
     _check(st, where)
 
 
@@ -569,7 +572,7 @@ def kv_cache_gather(cache, page_table, cu, k=None, v=None, total=None, stream=No
     _ints(where, page_table, n, max_pages)
     st = load().wanvae_kv_cache_gather(cache.ref, page_table.data_ptr(), max_pages, cu.data_ptr(),
                                        n, T, k.data_ptr(), ks, v.data_ptr(), vs,
-                                       _raw_stream(stream, dev))
+                                       _raw_stream(where, stream, dev))
     _check(st, where)
     return k, v
 
@@ -607,7 +610,7 @@ def paged_attention(q, cache, lens, page_table, out=None, workspace=None, scale=
                                        page_table.data_ptr(), max_pages, n, Hq,
                                        D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
                                        workspace.data_ptr(), workspace.nbytes,
-                                       _raw_stream(stream, dev))
+                                       _raw_stream(where, stream, dev))
     _check(st, where)
     return out
 
@@ -642,6 +645,6 @@ def gated_residual_norm(x, f, gamma_post=None, gate=None, gamma_pre=None, tokens
     st = load().wanvae_gated_residual_norm(
         x.data_ptr(), f.data_ptr(), _raw(gamma_post), _raw(gate), tokens_per_gate,
         _raw(gamma_pre), y.data_ptr(), _raw(n), BF16 if dtype == torch.bfloat16 else F32,
-        tokens, C, residual_scale, eps, _raw_stream(stream, dev))
+        tokens, C, residual_scale, eps, _raw_stream(where, stream, dev))
     _check(st, where)
     return y, n
