@@ -118,3 +118,16 @@ def test_cache_offsets_behind_the_rows_are_reported(cuda_lib, dtype):
         cuda_lib.sync_status()
     for got, want in ((out_k, want_k), (out_v, want_v)):
         assert torch.equal(got[:20], want[:20]) and torch.all(got[20:] == 7.0)
+
+
+def test_paged_workspace_with_gaps_is_refused(cuda_lib):
+    """Its bytes would not be where its elements are."""
+    cache = cuda_lib.make_kv_cache(3, 16, 2, 64)
+    q, table, lens = normal(gen(3), 1, 2, 64), ints([[0, 1, 2]]), ints([0])
+    ws = cuda_lib.make_paged_attention_workspace(q, cache)
+    cuda_lib.paged_attention(q, cache, lens, table, workspace=ws)
+    cuda_lib.sync_status()
+    with pytest.raises(cuda_lib.WanvaeError) as ei:
+        cuda_lib.paged_attention(q, cache, lens, table,
+                                 workspace=torch.cat([ws, ws])[::2])
+    assert ei.value.status == cuda_lib.ERR_INVALID_ARG

@@ -598,6 +598,7 @@ def paged_attention(q, cache, lens, page_table, out=None, workspace=None, scale=
         out = _result(stream, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
     if workspace is None:
         workspace = _on_stream(stream, make_paged_attention_workspace, q, cache)
+    _fit(where, workspace.is_contiguous())
     qs, os_ = _heads(where, q), _heads(where, out)
     shape = q.shape
     n, Hq, D = shape
