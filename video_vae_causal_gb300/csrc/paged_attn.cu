@@ -744,11 +744,13 @@ paged_join_kernel(const PagedArgs p, int block_heads) {
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const float f = at + k * kW < n ? weight[at + k * kW] : 0.f;
+            // (behind the last part: 0 times 0, not times what was loaded, which may be infinite)
+            const bool in = at + k * kW < n;
+            const float f = in ? weight[at + k * kW] : 0.f;
 #pragma unroll
             for (int e = 0; e < E / 2; ++e) {
-                acc[2 * e] = fmaf(f, x[k][e].x, acc[2 * e]);
-                acc[2 * e + 1] = fmaf(f, x[k][e].y, acc[2 * e + 1]);
+                acc[2 * e] = fmaf(f, in ? x[k][e].x : 0.f, acc[2 * e]);
+                acc[2 * e + 1] = fmaf(f, in ? x[k][e].y : 0.f, acc[2 * e + 1]);
             }
         }
     }
