@@ -203,3 +203,30 @@ def test_gated_norm_of_many_tokens(cuda_lib, dtype, C):
     assert ((y.double() - ry).abs() <= u * ry.abs() + 2.0 ** -20 * parts).all()
     scale = C ** 0.5 / ry.norm(dim=-1, keepdim=True) * gn.double()
     assert ((m.double() - rm).abs() <= u * rm.abs() + 2.0 ** -19 * parts * scale.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("C", [32, 384, 4096])
+def test_gated_norm_rows_not_finite(cuda_lib, dtype, C):
+    """A NaN in a row makes its norm NaN, and with it the whole normed row; an infinity makes
+    it infinite: NaN where it lies, zeros elsewhere.  Other rows are as ever."""
+    g = gen(37)
+    n = 40
+    x, f = normal(g, n, C, dtype=dtype), normal(g, n, C, dtype=dtype)
+    gp, gn = (torch.rand(C, generator=g, device=DEV) + 0.5 for _ in range(2))
+    f[3, 5], f[7, C - 1] = math.nan, math.inf
+    x[11, 2], x[13, 9] = math.nan, -math.inf
+    y, m = cuda_lib.gated_residual_norm(x, f, gp, None, gn)
+    cuda_lib.sync_status()
+    ry, rm, parts = norm_reference(x, f, gp, None, 1, 1.0, gn, 1e-12)
+    u = U if dtype == torch.bfloat16 else 2.0 ** -24
+    scale = C ** 0.5 / ry.norm(dim=-1, keepdim=True) * gn.double()
+    for got, want, bar in ((y.double(), ry, u * ry.abs() + 2.0 ** -20 * parts),
+                           (m.double(), rm, u * rm.abs() + 2.0 ** -19 * parts * scale.abs())):
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)])
+        fin = torch.isfinite(want) & torch.isfinite(bar)
+        assert ((got - want).abs() <= bar)[fin].all()
+        still = torch.ones(n, dtype=torch.bool, device=DEV)
+        still[[3, 7, 11, 13]] = False
+        assert fin[still].all()

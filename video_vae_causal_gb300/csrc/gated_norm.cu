@@ -60,6 +60,13 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float *part) {
     return s;
 }
 
+// What a row of sum of squares `ss` is multiplied by: NaN where the row holds one (the
+// clamp's maximum would drop it, and give the row's other channels a norm of eps).
+__device__ __forceinline__ float row_scale(float ss, float sqrt_c, float eps) {
+    const float s = nact_scale(ss, sqrt_c, eps);
+    return ss == ss ? s : ss;
+}
+
 template <bool F32>
 struct Vec {
     static constexpr int E = F32 ? 4 : 8;
@@ -126,7 +133,7 @@ gated_norm_kernel(const GatedArgs a) {
                 for (int k = 0; k < E; ++k) ss = fmaf(t[k], t[k], ss);
             }
             ss = row_sum(ss, a.tpr, part[0]);
-            scale *= nact_scale(ss, a.sqrt_c, a.eps);
+            scale *= row_scale(ss, a.sqrt_c, a.eps);
         }
         const float *gate = a.gate && there ? a.gate + (uint64_t)(row / a.per_gate) * a.V * E
                                             : nullptr;
@@ -159,7 +166,7 @@ gated_norm_kernel(const GatedArgs a) {
         }
         if (a.g_pre) {
             ss = row_sum(ss, a.tpr, part[1]);
-            const float rn = nact_scale(ss, a.sqrt_c, a.eps);
+            const float rn = row_scale(ss, a.sqrt_c, a.eps);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int j = sub + i * a.tpr;
