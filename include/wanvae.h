@@ -238,6 +238,7 @@ wanvae_status wanvae_frame_attention(const void *x, const float *gamma, const vo
  *   n_heads : a multiple of n_kv_heads, at most 128 times as many; head h
  *             reads kv head h / (n_heads / n_kv_heads)
  *   head_dim : 64 or 128.  Strides: multiples of 8, at least a token's width.
+ * n_seq, total_q and total_k are at least 1.  out lies over none of the inputs.
  * Scores and sums in fp32; the weights are rounded to bf16 for the product.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_packed_attention(const void *q, int64_t q_stride, const void *k,
@@ -278,7 +279,7 @@ typedef struct {
  * No two tokens of a call may lie in the same slot (sequences may share pages that
  * the call does not write).  A token whose position or page lies outside the page
  * table or the cache, or whose sequence ends behind total, is not written, and
- * wanvae_sync_status reports WANVAE_ERR_CUDA.
+ * wanvae_sync_status reports WANVAE_ERR_CUDA.  n_seq and total are at least 1.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_kv_cache_append(const wanvae_kv_cache *cache, const void *k,
                                      int64_t k_stride, const void *v, int64_t v_stride,
@@ -309,12 +310,17 @@ wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t
  *   workspace : wanvae_paged_attention_workspace_size() bytes, 256-byte aligned,
  *            contents ignored; not shared by calls that overlap on the GPU.
  * The cache's rows are split over the whole GPU by their number, so the result
- * of a sequence depends on the other sequences' lengths in its last bits.
- * Scores and sums in fp32.  The weights are rounded for the product: to bf16 over a bf16
- * cache (2^-8 relative); over an E4M3 cache a weight times its value row's scale to
- * 2^-11, or to 2^-25 of the sequence's largest such product, where that is more: value
- * rows of scales 2^20 and more below those of the rows that count most lose bits.  Rows of
- * zeros take no part in that, if their scale is 1 (as wanvae_kv_cache_append writes them).
+ * of a sequence depends on the other sequences' lengths in its last bits.  How they are
+ * split, and which kernel reads them, is chosen by how far the page table reaches
+ * (max_pages * page_size): a table much wider than the sequences are long costs some time.
+ * Scores and sums in fp32.  (Over an E4M3 cache the largest magnitudes of a query and of a
+ * key row, multiplied with each other and with scale, have to stay below 2^127, even
+ * where they meet zeros: beyond it a score of zero may become NaN.)  The weights are
+ * rounded for the product: to bf16 over a bf16 cache (2^-8 relative); over an E4M3 cache a
+ * weight times its value row's scale to 2^-11, or to 2^-25 of the sequence's largest such
+ * product, where that is more: value rows of scales 2^20 and more below those of the rows
+ * that count most lose bits.  Rows of zeros take no part in that, if their scale is 1 (as
+ * wanvae_kv_cache_append writes them).
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA. */
 size_t wanvae_paged_attention_workspace_size(int64_t n_heads, int64_t n_kv_heads,
                                              int64_t head_dim);
@@ -334,7 +340,8 @@ wanvae_status wanvae_paged_attention(const void *q, int64_t q_stride,
  *   gate       : fp32 [ceil(n_tokens / tokens_per_gate)][C], or NULL (one);
  *                token i has row i / tokens_per_gate (a frame's gate, say)
  *   gamma_pre  : fp32 [C], or NULL together with n: y alone is written
- *   Math in fp32, n from y before it is rounded; bf16 rounds to nearest-even.
+ *   Math in fp32 (a row's sum of squares too: norms of up to 2^63), n from y before it is
+ *   rounded; bf16 rounds to nearest-even.  A NaN in a row makes its norm NaN.
  * Errors: INVALID_ARG (as wanvae_rmsnorm_silu), MISALIGNED, CUDA. */
 wanvae_status wanvae_gated_residual_norm(const void *x, const void *f, const float *gamma_post,
                                          const float *gate, int64_t tokens_per_gate,

@@ -17,9 +17,10 @@
 // contiguous, which is how attention over the cache reads them.  Both passes
 // move each row once (2 D bytes on one side, D + 1 on the other) and are bound
 // by HBM: 73513 tokens of 8 heads of 128 read back take 78 us (5.8 TB/s, 0.86 of
-// the measured copy rate), 16384 tokens written 27 us (3.7 TB/s, 0.55: a warp has
-// five tokens, whose places, loads and rows' maxima it waits for in turn; loading the
-// next pass's rows as each is used spilled and took 29 us).  A row takes D / 8 lanes with
+// the measured copy rate), 16384 tokens written 27 us (3.7 TB/s, 0.55: 2.7 tokens a
+// warp, so that some have two and some three, and it waits for their places, loads and
+// rows' maxima one token after another; loading the next pass's rows as each is used
+// spilled and took 29 us).  A row takes D / 8 lanes with
 // one 16-byte vector of bf16 each; a warp keeps the rows of a token's heads together and
 // takes tokens in a row, so that a token's page is looked up once for all heads and its
 // sequence once for the tokens that follow it.

@@ -30,13 +30,15 @@
 // unrounded P.  (Taking the first half's weights from the maximum so far while the
 // turn's is found changed nothing: 333 us.)
 //
-// What bounds it: for D = 128 the tensor core, 2048 cycles of MMAs for 128 keys of both
-// tiles (Q K^T reads both operands from shared memory, 48 cycles an MMA of 64 columns, not
-// 16) of about 2900; 16 query and 4 kv heads over causal prompts of 8192, 5003, 188 and
-// 3001 tokens: 304 us, 1.36 PFLOP/s, 0.70 of the measured matrix rate.  For D = 64 the
-// threads: 128 keys of both tiles are 1460 cycles of exponentials, sums, maxima and
-// roundings on an SM quarter (1024 of them MUFU's) of about 2300; 21 frames of 6240
-// tokens, 6 heads, full: 1190 us, 1.05 PFLOP/s, 0.54.
+// What bounds it: for D = 128 the tensor core, 2048 cycles of arithmetic for 128 keys of both
+// tiles of about 2900 (the tensor pipe is 61 % active; Q K^T, half of it, also reads both
+// operands from shared memory); 16 query and 4 kv heads over causal prompts of 8192, 5003,
+// 188 and 3001 tokens: 301 us, 1.38 PFLOP/s, 0.71 of the measured matrix rate.  For D = 64
+// nothing alone: 128 keys of both tiles take about 2300 cycles, of which an SM quarter issues
+// 1460 (exponentials, sums, maxima and roundings, 1024 of them MUFU's) and the tensor core
+// works 1024; the rest is what two warps a scheduler leave bare of the chain from S in TMEM
+// over the maximum and the exponentials back to TMEM.  21 frames of 6240 tokens, 6 heads,
+// full: 1195 us, 1.05 PFLOP/s, 0.54.
 //
 // Masked scores are replaced, never added to, so nothing in a masked key
 // reaches a row.  A masked value's weight is zero, but 0 * NaN is not: of the blocks

@@ -3,9 +3,9 @@
 //
 //     out[b, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q[b, h] . k_j)
 //
-// over the lens[b] cached rows of kv head h / G.  Every row is read once for
-// the G query heads that share it, so the work is G multiply-adds a cache
-// byte or less and the bound is HBM.
+// over the lens[b] cached rows of kv head h / G.  Every row is read once for up to
+// 16 of the G query heads that share it (once more for every 16 after that), so the work
+// is 16 multiply-adds a cache byte or less and the bound is HBM.
 //
 // Split.  The rows of one (sequence, kv head) are cut into units of 64 or 128; the
 // units of the whole batch, laid end to end, are dealt to the CTAs in equal
@@ -40,11 +40,14 @@
 // is seldom: rows of e = 0 alone (any rows: 1.6 us more of 18, for 28803 rows of one kv head
 // over as many CTAs).
 //
+// Over 16-bit rows the weights round to bf16, the type that the values have (an MMA's operands
+// share one), and carry no scales: r is m.
+//
 // What bounds it: HBM for 16-bit rows (64 sequences of 17 to 8192 rows, 8 kv heads of 4 query
-// heads of 128: 169 us, 6.1 TB/s, 0.90 of the measured copy rate; of 64: 89 us, 5.7 TB/s),
-// the conversions for 8-bit ones (of 64: 84 us, 3.0 TB/s; one sequence of 131040 rows, 8
-// heads of 8 of 128: 60 us, 4.5 TB/s; about 470 warp instructions for 16 rows of 128, half
-// as many for 64).  Where a long 8-bit cache of 128-element heads
+// heads of 128: 174 us, 6.2 TB/s, 0.91 of the measured copy rate; of 64: 93 us, 5.8 TB/s),
+// the conversions for 8-bit ones (of 64: 89 us, 3.1 TB/s; one sequence of 131040 rows, 8
+// heads of 8 of 128: 60 us, 4.5 TB/s, of 16: 66 us; about 470 warp instructions for 16 rows of
+// 128, half as many for 64).  Where a long 8-bit cache of 128-element heads
 // would wait for those, the tensor core reads it as it is: paged_attn_tc.cu.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -64,11 +67,12 @@ constexpr int kJoinThreads = 128;
 constexpr float kLag = 4.f;  // how far a score may pass m before m moves
 // Keys of an item (a sequence and a block of heads), as far as the page table reaches, up
 // to which a CTA takes an item whole and no join follows; twice this where a quarter of
-// the CTAs have one, four times where all have.  Shared / apart, in us, tables of 16-row
-// pages, 8-bit rows of 128: 8 items of 256 rows 8.2 / 6.1, of 512 8.3 / 8.6, of 1024 8.8 /
-// 13.8; 128 of 1024 20.0 / 18.8, of 2048 27.0 / 32.4; 320 of 1 to 2000 42.2 / 32.6, 512
-// 53.8 / 47.2, 1600 130 / 107; 16-bit rows of 128: 8 of 256 7.7 / 6.2, 128 of 512 17.6 / 13.5,
-// 512 of 1 to 1000 48.6 / 30.8.
+// the CTAs have one, four times where all have.  Shared / apart, in us with the host's call,
+// tables of 16-row pages, 8-bit rows of 128: 8 items of 256 rows 10.8 / 8.9, of 512 11.3 /
+// 9.4, of 1024 11.0 / 14.9; 128 of 1024 19.4 / 18.8, of 2048 25.9 / 33.6; 320 of 1 to 2000
+// 31.3 / 33.0, 512 42.3 / 48.3, 1600 116 / 108 (four times is early for a few hundred ragged
+// items); 16-bit rows of 128: 8 of 256 11.2 / 8.7, 128 of 512 15.3 / 12.5, 512 of 1 to 1000
+// 32.7 / 31.9.
 constexpr int64_t kApartBytes = 64 << 10;
 
 // D += A B, 16 x 8 x 16, fp16 or bf16 in, fp32 out.
@@ -111,9 +115,9 @@ struct Shape {
     static constexpr int kCtas = 2;
     static constexpr int kUnit = 16 * NG * kWarps;   // cache rows of a unit
     // An item's queries, first loads and join cost about two units: 32 sequences of 50 to
-    // 6000 rows, 4 kv heads, 16-bit rows of 128, take 45.2, 33.7 and 33.7 us with 0, 2 and
-    // 4 counted, 64 of 17 to 8192 rows, 8 kv heads, 174, 169 and 167 (8-bit rows of 64: 96,
-    // 84 and 88).
+    // 6000 rows, 4 kv heads, 16-bit rows of 128, take 44.1, 40.7 and 40.8 us with 0, 2 and
+    // 4 counted, 64 of 17 to 8192 rows, 8 kv heads, 178, 174 and 175 (8-bit rows of 64: 100,
+    // 89 and 91).
     using U = Units<kUnit, 2>;
     static constexpr int kHalf = 16 * RB;            // bytes of a group's keys, or values
     static constexpr int kTurn = NG * 2 * kHalf;     // bytes of a warp's turn
@@ -774,12 +778,13 @@ int head_block(int G) { return G <= 8 ? 8 : 16; }
 
 // Whether the tcgen05 kernel takes the call: 8-bit rows of 128 elements.  It reads faster but
 // begins an item later, and its threads' work grows with the query heads of a kv head.
-// Measured, here (in shares) / there, in us, 8 kv heads: long tables, one sequence of 16384 rows 17.0 / 15.2
-// (4 query heads a kv head) and 18.1 / 18.9 (8), of 131040 58.6 / 48.7 and 60.2 / 52.0, 64
-// of 17 to 8192 122 / 89 and 135 / 104; short ones, 64 of 300 rows 23.4 / 28.9 and 29.1 /
-// 38.9, 64 of 1000 40.2 / 38.2 and 45.8 / 54.7, one of 300 8.2 / 10.9; 16 query heads,
-// one of 131040 68.4 / 79.8 (8 of them a turn there would read the cache twice).  The host
-// knows how far the page table reaches, not the lengths.
+// Measured, here / there, in us, 8 kv heads: long tables (here in shares), one sequence of
+// 16384 rows 16.9 / 14.7 (4 query heads a kv head) and 17.5 / 18.7 (8), of 131040 59.4 / 48.8
+// and 60.2 / 53.1, 64 of 17 to 8192 114 / 94 and 120 / 113; short ones (an item a CTA), 64 of
+// 300 rows 19.7 / 30.8 and 22.0 / 39.9, 64 of 1000 37.6 / 41.5 and 39.7 / 54.3, one of 300
+// 9.1 / 10.8; 16 query heads, one of 131040 68.4 / 79.8 when it was tried (8 of them a turn
+// there would read the cache twice).  The host knows how far the page table reaches, not
+// the lengths.
 bool on_tc(const KvCacheSpec &c, int G, int max_pages, int n_seq) {
     const int64_t rows = (int64_t)max_pages << c.log2_page;
     return c.e4m3 && c.D == 128 && G <= 8 && rows > 2048 &&

@@ -196,7 +196,7 @@ int paged_ways(const PagedArgs &a, int rows, int most);
 // The tcgen05 kernel (paged_attn_tc.cu): 8-bit rows of 128 elements, at most 8 query
 // heads a kv head.  An item costs about two units besides its own: the queries' way into
 // shared memory, the first maximum, the joined output (64 sequences of 17 to 8192
-// rows, 8 kv heads of 8 query heads: 113, 104 and 104 us with 1, 2 and 3 counted).
+// rows, 8 kv heads of 8 query heads: 118, 113 and 113 us with 1, 2 and 3 counted).
 // *block_heads: the heads of a partial result.
 using TcUnits = Units<256, 2>;
 cudaError_t launch_paged_tc(PagedArgs &a, const KvCacheSpec &cache, const LaunchCtx &ctx,

@@ -79,7 +79,7 @@ enum : int { kOwnQs = 0, kOwnTop = 8, kOwnM = 16, kOwnR = 24, kOwnF = 32, kOwnFl
              kOwnRl = 56, kOwnSize = 64 };
 
 // HP: query heads of an item, at most (4 or 8: a thread's work grows with them, and
-// with 8 in place of 4 the sequences below take 104 us instead of 89).
+// with 8 in place of 4 the batch above takes 108 us instead of 94).
 template <int HP>
 struct Cfg {
     static constexpr int N1 = 2 * HP < 16 ? 16 : 2 * HP;         // columns of S
