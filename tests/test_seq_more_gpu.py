@@ -230,3 +230,33 @@ def test_gated_norm_rows_not_finite(cuda_lib, dtype, C):
         still = torch.ones(n, dtype=torch.bool, device=DEV)
         still[[3, 7, 11, 13]] = False
         assert fin[still].all()
+
+
+@pytest.mark.parametrize("D,group", [(64, 4), (64, 12), (128, 2), (128, 8), (128, 12)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_paged_bits_do_not_depend_on_the_call_before(cuda_lib, D, group, wide):
+    """Short sequences leave most of a unit's places unread: what an earlier call left in
+    shared memory there (scales of 2^-100, of 2^100) changes no bit of the result."""
+    hkv, page = 8, 16
+    lens = [(37 * i) % 200 for i in range(100)]
+    cache, table, _, _ = fill(cuda_lib, lens, page, hkv, D, E4M3, seed=40)
+    q = normal(gen(41), len(lens), hkv * group, D)
+    if wide:
+        table = widened(table, page, hkv)
+    before = []
+    for size in (2.0 ** -95, 2.0 ** 105):
+        def edit(k, v):
+            v *= size
+            k *= 2.0 ** -10
+        c, t, _, _ = fill(cuda_lib, [2000] * 20, page, hkv, D, E4M3, seed=42, edit=edit)
+        if wide:
+            t = widened(t, page, hkv)
+        before.append((normal(gen(43), 20, hkv * group, D), c, ints([2000] * 20), t))
+    got = []
+    for args in (None, *before, *before):
+        if args is not None:
+            cuda_lib.paged_attention(*args)
+        got.append(cuda_lib.paged_attention(q, cache, ints(lens), table))
+    cuda_lib.sync_status()
+    for a in got[1:]:
+        assert torch.equal(got[0], a)

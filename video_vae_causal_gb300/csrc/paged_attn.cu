@@ -389,9 +389,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
                     }
             }
             uint32_t pb[NH][NG][2];
-            // (least_e: see paged_attn.cuh)
+            // (least_e: see paged_attn.cuh; rows that are not there, whose scales are whatever
+            // lay in the queue's place, ask for nothing)
             bool low = false;
             if (Q8) {
+                if (rows != (NG == 2 ? 0x1010 : 0x10)) {
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (8 * j + S::row_of(2 * t + c) >= ((rows >> (8 * i)) & 0xff))
+                                    ve[i][j][c] = 128.f;
+                }
                 float x = INFINITY;
 #pragma unroll
                 for (int i = 0; i < NG; ++i)

@@ -624,7 +624,7 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
                 const float kf = __uint_as_float((uint32_t)ex[0] << 23);
                 ve[k] = (float)ex[kUnit] - 127.f;
                 there[k] = row < u.rows && !((u.missing >> (row >> log2_box)) & 1u);
-                moves |= ve[k] < least_e;
+                moves |= there[k] && ve[k] < least_e;
                 uint32_t raw[C::N1];
                 tmem_read(trow + C::s_col(buf.i) + 32u * k, raw);
                 // scores in log2 units
