@@ -45,8 +45,8 @@
 //
 // What bounds it: HBM for 16-bit rows (64 sequences of 17 to 8192 rows, 8 kv heads of 4 query
 // heads of 128: 174 us, 6.2 TB/s, 0.91 of the measured copy rate; of 64: 93 us, 5.8 TB/s),
-// the conversions for 8-bit ones (of 64: 89 us, 3.1 TB/s; one sequence of 131040 rows, 8
-// heads of 8 of 128: 60 us, 4.5 TB/s, of 16: 66 us; about 470 warp instructions for 16 rows of
+// the conversions for 8-bit ones (of 64: 91 us, 3.0 TB/s; one sequence of 131040 rows, 8
+// heads of 8 of 128: 60 us, 4.5 TB/s, of 16: 67 us; about 470 warp instructions for 16 rows of
 // 128, half as many for 64).  Where a long 8-bit cache of 128-element heads
 // would wait for those, the tensor core reads it as it is: paged_attn_tc.cu.
 #include <cuda.h>
