@@ -31,14 +31,14 @@
 // 8-bit elements become fp16, exactly, on their way into the MMA (mma.sync of e4m3 operands
 // has no rate of its own here).  A query is scaled by a power of two that brings its
 // largest element to exponent 14, where bf16's 8 bits stay whole down to 2^-31 of it
-// and below that round to within 2^-39 of it; weights round once to fp16.  A key row's scale multiplies its score; a value row's scale 2^e joins the
-// exponent of its weight, w_j = 2^(s_j + e_j - m) with m the running maximum of s_j + e_j,
-// so that weights stay in fp16's upper range whatever the scales are, while the sum takes
-// 2^(s_j - r) in fp32, r the running maximum of the scores alone (see paged_attn.cuh).  A
-// weight is off by 2^-11 of itself or, where that is more, by 2^-25 of the largest 2^(s + e);
-// rows of zeros (scale 1) do not count there.  They are looked for where m would move, which
-// is seldom: rows of e = 0 alone (any rows: 1.6 us more of 18, for 28803 rows of one kv head
-// over as many CTAs).
+// and below that round to within 2^-39 of it; weights round once to fp16.  A key row's
+// scale multiplies its score; a value row's scale 2^e joins the exponent of its weight,
+// w_j = 2^(s_j + e_j - m) with m the running maximum of s_j + e_j, so that weights stay in
+// fp16's upper range whatever the scales are, while the sum takes 2^(s_j - r) in fp32, r the
+// running maximum of the scores alone (see paged_attn.cuh).  A weight is off by 2^-11 of
+// itself or, where that is more, by 2^-25 of the largest 2^(s + e); rows of zeros (scale 1) do
+// not count there.  They are looked for where m would move, which is seldom, among rows of
+// e = 0 alone (as in the tcgen05 kernel, where the values may still be on their way).
 //
 // Over 16-bit rows the weights round to bf16, the type that the values have (an MMA's operands
 // share one), and carry no scales: r is m.
