@@ -239,7 +239,8 @@ wanvae_status wanvae_frame_attention(const void *x, const float *gamma, const vo
  *             reads kv head h / (n_heads / n_kv_heads)
  *   head_dim : 64 or 128.  Strides: multiples of 8, at least a token's width.
  * n_seq, total_q and total_k are at least 1.  out lies over none of the inputs.
- * Scores and sums in fp32; the weights are rounded to bf16 for the product.
+ * Scores and sums in fp32 (a sequence's keys times its largest value stay below 2^119);
+ * the weights are rounded to bf16 for the product.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_packed_attention(const void *q, int64_t q_stride, const void *k,
                                       int64_t k_stride, const void *v, int64_t v_stride, void *out,
@@ -315,7 +316,8 @@ wanvae_status wanvae_kv_cache_gather(const wanvae_kv_cache *cache, const int32_t
  * (max_pages * page_size): a table much wider than the sequences are long costs some time.
  * Scores and sums in fp32.  (Over an E4M3 cache the largest magnitudes of a query and of a
  * key row, multiplied with each other and with scale, have to stay below 2^127, even
- * where they meet zeros: beyond it a score of zero may become NaN.)  The weights are
+ * where they meet zeros: beyond it a score of zero may become NaN; over a bf16 cache the
+ * rows times the largest value stay below 2^123.)  The weights are
  * rounded for the product: to bf16 over a bf16 cache (2^-8 relative); over an E4M3 cache a
  * weight times its value row's scale to 2^-11, or to 2^-25 of the sequence's largest such
  * product, where that is more: value rows of scales 2^20 and more below those of the rows
