@@ -163,8 +163,8 @@ constexpr float kLowest = -FLT_MAX;
 constexpr float kSumLag = 60.f;  // (2^31 rows of 2^60 stay in fp32's range)
 
 // The output from sums relative to m and r, zero where no row counted: acc / sum *
-// 2^(m - r), this last in two factors, as m - r is up to 120 + kSumLag.  (Rows of 16 bits have
-// no scales, and one reference.)
+// 2^(m - r), this last in two factors, as m - r is up to 120 + kSumLag (over 4 bits on tcgen05 up to
+// 32 more: kStep there, and m set ahead).  (Rows of 16 bits have no scales, and one reference.)
 __device__ __forceinline__ float half_factor(float m, float r) { return exp2_fast(0.5f * (m - r)); }
 template <bool Q8>
 __device__ __forceinline__ float output_of(float acc, float sum, float half) {

@@ -98,6 +98,10 @@ struct Unit {
 // kLast alone where it has one), whether a range holds it whole, the end of all.
 enum : int { kFirst = 1, kSecond = 2, kLast = 4, kLastBut1 = 8, kWhole = 16, kEnd = 32 };
 
+// How far a score may pass m in one unit, over 4 bits, without the sum's reference r moving too
+// (2^31 rows of 2^(kSumLag + kStep) stay in fp32's range).
+constexpr float kStep = 30.f;
+
 // What a softmax warp keeps for the heads of its item, in shared memory (own[kind + head]):
 // the queries' factors; the largest s + e where m moves; m and r (paged_attn.cuh; m is the
 // group's, r the warp's); the factors that O and the sums go on with; the sum at the item's
@@ -1058,8 +1062,15 @@ __device__ void softmax(const PagedArgs &p, int w, uint8_t *smem, uint32_t tmem,
             }
             float top = -INFINITY, stop = -INFINITY;  // of s + e, of s; head hl's
             // (4 bits: m alone moves, as a rule, and the weights have shown how far.  The warp's
-            // r may stay behind, as long as no row asks for it.)
-            const bool known = C::Q4 && !__any_sync(0xffffffffu, low || fresh ||
+            // r may stay behind, where no row asks for it and no row's s + e passes m by more than
+            // 1 + kStep: with e >= least_e = m - r - (kSumLag - 1), s - r is at most kSumLag +
+            // kStep then, and m - r at most 120 more.  From the next unit on least_e goes by
+            // the new m.  A higher step would take the sum to infinity: r moves with m.)
+            bool far = false;
+            if (C::Q4 && !fresh)
+#pragma unroll
+                for (int h = 0; h < HP; ++h) far |= tops[h] > 8.f + kStep;
+            const bool known = C::Q4 && !__any_sync(0xffffffffu, low || far || fresh ||
                                                                      own[kOwnM + hl] == kLowest ||
                                                                      own[kOwnR + hl] == kLowest);
             if (known) {
