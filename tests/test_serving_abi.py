@@ -247,3 +247,12 @@ def test_tensors_off_the_device_are_refused(lib):  # noqa: F811
         with pytest.raises(wanvae.WanvaeError) as ei:
             call()
         assert ei.value.status == ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype,code", [(torch.uint8, 127 - 94), (torch.float8_e4m3fn, 127)])
+def test_an_empty_caches_rows_have_the_scale_of_zeros(dtype, code):
+    cache = wanvae.make_kv_cache(2, 16, 3, 64, dtype=dtype, device="cpu")
+    for e in (cache.k_exp, cache.v_exp):
+        assert (e.view(torch.uint8) == code).all()
+    assert all((t.view(torch.uint8) == 0).all() for t in cache.tensors()
+               if t is not cache.k_exp and t is not cache.v_exp)

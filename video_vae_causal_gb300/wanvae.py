@@ -558,7 +558,9 @@ def make_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e
                         device=device).view(dtype) for _ in range(2))
     if dtype not in (torch.float8_e4m3fn, torch.uint8):
         return KVCache(k, v)
-    ke, ve = (torch.full(rows, 127, dtype=torch.uint8, device=device)
+    # (the scales that rows of zeros are written with: 1, in 4 bits the smallest)
+    zeros = 127 - 94 if dtype == torch.uint8 else 127
+    ke, ve = (torch.full(rows, zeros, dtype=torch.uint8, device=device)
               .view(torch.float8_e8m0fnu) for _ in range(2))
     if dtype != torch.uint8:
         return KVCache(k, v, ke, ve)
