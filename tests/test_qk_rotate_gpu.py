@@ -205,3 +205,18 @@ def test_offsets_beyond_32_bits(cuda_lib):
     want, size = definition(x, gamma, angles(pos, rotary), False)
     check(got, want, size)
     assert torch.equal(q, got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_negative_frequencies_turn_back(cuda_lib, dtype):
+    """-f at a position is f at the negated one, bit for bit, however far it lies."""
+    freq = [0.3, 1e-3, 1e-7, 2.5, 1.0, 0.7311, 1e-12, 1234.5678]
+    pos = torch.tensor([1, 12345, 99999, 2 ** 31 - 1, 2 ** 31 - 1000, 1 - 2 ** 31, -7],
+                       dtype=torch.int32, device=DEV)
+    x = normal(gen(6), len(pos), 2, 64, dtype=dtype)
+    back, _ = cuda_lib.qk_norm_rotate(x, None, pos, cuda_lib.Rotary([8], inv_freq=[-f for f in freq]))
+    want, _ = cuda_lib.qk_norm_rotate(x, None, -pos, cuda_lib.Rotary([8], inv_freq=freq))
+    cuda_lib.sync_status()
+    assert torch.equal(back, want)
+    angle = angles(pos, cuda_lib.Rotary([8], inv_freq=[-f for f in freq]))
+    check(back, *definition(x, None, angle, False))

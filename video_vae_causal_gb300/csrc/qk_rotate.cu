@@ -326,13 +326,16 @@ cudaError_t pick(RotateArgs &a, bool f32, bool near, const LaunchCtx &ctx) {
     return near ? launch<D, false, true>(a, ctx) : launch<D, false, false>(a, ctx);
 }
 
-// f radians in turns, without the whole ones, times 2^64: 1 / (2 pi) in two parts, so that
-// a position of 31 bits leaves the product's upper half exact (f up to 2^20).
+// f radians in turns, without the whole ones, times 2^64, off by less than 2 (f up to 2^20; 1 / (2 pi)
+// in two parts): a position of 31 bits then leaves the angle within 2^-31 of a turn.  A negative
+// f is its magnitude turned back, as the fraction of a small negative product lies near 1,
+// where 53 bits hold 1024 times less of it.
 uint64_t fraction_of_turn(double f) {
     const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
-    const double p = f * hi, rest = fma(f, hi, -p) + f * lo;
-    const double frac = p - floor(p);
-    return (frac < 1.0 ? (uint64_t)(frac * 0x1p64) : 0) + (uint64_t)(int64_t)(rest * 0x1p64);
+    const double a = fabs(f), p = a * hi, rest = fma(a, hi, -p) + a * lo;
+    const double frac = p - floor(p);  // (exact)
+    const uint64_t turn = (uint64_t)(frac * 0x1p64) + (uint64_t)(int64_t)(rest * 0x1p64);
+    return f < 0.0 ? 0 - turn : turn;
 }
 
 }  // namespace
