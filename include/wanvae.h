@@ -317,7 +317,10 @@ wanvae_status wanvae_kv_cache_write(const wanvae_kv_cache *cache, const void *k,
 
 /* The free pages of a cache as a stack (device, caller-owned): free_pages int32 [n_pages]
  * (every page of the cache), of which the first n_free[0] are free, the next to be
- * taken last.  page_size as the cache's. */
+ * taken last.  page_size as the cache's.  A page is free or one sequence's, once: the pool
+ * counts no users.  (Pages that several sequences read, a common prefix's, have to stay out of
+ * it, and such a sequence is not released through it: each release would put them back, and
+ * two sequences would then be given the same page.) */
 typedef struct {
     int32_t *free_pages, *n_free;
     int64_t n_pages, page_size;
@@ -361,6 +364,8 @@ wanvae_status wanvae_kv_pages_extend(const wanvae_kv_page_pool *pool, const int3
 /* The pages of every sequence with done[s] != 0 (uint8 [n_seq], device) go back onto the
  * stack, in the order of the sequences and of their pages, and its length becomes 0.
  *   lens_out, n_free_out : as for wanvae_kv_pages_extend
+ * No page is in two of these sequences' tables, nor in that of one that goes on (see
+ * wanvae_kv_page_pool; not checked).
  * A sequence whose length is negative or passes the page table keeps it, and pages beyond
  * the stack's size are not put back; both are reported by wanvae_sync_status as
  * WANVAE_ERR_CUDA, as is a page outside the pool (which goes back as it is).

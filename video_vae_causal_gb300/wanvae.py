@@ -609,7 +609,8 @@ def kv_cache_write(cache, k, v, slots, stream=None):
 
 class KVPagePool:
     """The free pages of a cache over the caller's tensors: free int32 [n_pages], a stack of
-    which the first n_free[0] (int32 [1]) are free."""
+    which the first n_free[0] (int32 [1]) are free.  A page is free or one sequence's: pages
+    that several sequences read stay out of the pool (it counts no users)."""
 
     def __init__(self, free, n_free, page_size):
         where = "wanvae_kv_page_pool"
