@@ -303,13 +303,18 @@ qk_rotate_kernel(const __grid_constant__ RotateArgs a) {
 
 template <int D, bool F32, bool kNear>
 cudaError_t launch(RotateArgs &a, const LaunchCtx &ctx) {
-    static std::atomic<int> per_sm{0};
-    int occ = per_sm.load(std::memory_order_relaxed);
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> per_sm[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+    int occ = per_sm[dev].load(std::memory_order_relaxed);
     if (!occ) {
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &occ, qk_rotate_kernel<D, F32, kNear>, kThreads, 0);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, qk_rotate_kernel<D, F32, kNear>,
+                                                          kThreads, 0);
         if (e != cudaSuccess) return e;
-        per_sm.store(occ = std::max(1, occ), std::memory_order_relaxed);
+        per_sm[dev].store(occ = std::max(1, occ), std::memory_order_relaxed);
     }
     constexpr int G = 256 / D, kWarps = kThreads / 32;
     // whole tokens, where each warp has some; else pieces, of a head at the least
