@@ -390,7 +390,8 @@ typedef struct {
 } wanvae_rotary;
 
 /* The norm of every query and key head and its rotation by the token's position:
- *   n = RMS_norm(x; gamma) over the head's elements, as in the ResidualBlock (no SiLU)
+ *   n = RMS_norm(x; gamma) over the head's elements, as in the ResidualBlock (no SiLU):
+ *   x sqrt(head_dim) gamma / max(|x|, eps), eps a bound of the length, not a term of its root
  *   (y[a], y[b]) = (n[a] cos t - n[b] sin t, n[b] cos t + n[a] sin t) for each pair (a, b),
  *   t = position * inv_freq; elements of no pair are normed alone.
  *   q, q_out : [n_tokens][n_heads][head_dim] of type dt (bf16 or fp32), tokens q_stride /
@@ -401,8 +402,10 @@ typedef struct {
  *   An output may be its input, in place; else outputs lie over nothing else of the call
  *   (rows of them may lie between one another's in one buffer).
  *   head_dim : 64 or 128.  Strides: multiples of 8, at least a token's width.
- * Math in fp32 (a head's sum of squares too: norms of up to 2^63), angles to 2^-32 of a
- * turn whatever the position; one rounding at the end.  A NaN in a head makes its norm NaN.
+ * Math in fp32 (a head's sum of squares too: norms of up to 2^63); one rounding at the end.
+ * Angles are reduced to a turn to within 2^-31 of one, whatever the position; sines and cosines
+ * are off by less than 2^-22 in fp32 and 2^-20 in bf16 (absolute, so that a result is off by
+ * that of its pair's size besides its rounding).  A NaN in a head makes its norm NaN.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. */
 wanvae_status wanvae_qk_norm_rotate(const void *q, int64_t q_stride, const void *k,
                                     int64_t k_stride, const float *gamma_q, const float *gamma_k,

@@ -24,9 +24,10 @@
 // nothing, and need not be looked for.  A row with an
 // infinity or a NaN has the scale code 255 and reads as NaN throughout.
 //
-// In 4 bits 16384 tokens are written in 24 us (3.5 TB/s, 0.52: about 50 instructions for 8
-// elements; a lane with 8 of a block's 16, which then needs the other's maximum: 32 us), 73513
-// read back in 70.5 (5.4 TB/s, 0.80; a block a lane there: 72 to 83).
+// In 4 bits 16384 tokens are written in 24 us (3.5 TB/s, 0.52: 3.4 tokens a warp, so that some have
+// four, and a token's place, loads, maxima and stores one after another; the 50 or so instructions
+// for 8 elements are a quarter of it; a lane with 8 of a block's 16, which then needs the other's
+// maximum: 32 us), 73513 read back in 70.5 (5.4 TB/s, 0.80; a block a lane there: 72 to 83).
 //
 // Rows lie [page][head][slot][D]: the rows of one head and page are
 // contiguous, which is how attention over the cache reads them.  Both passes

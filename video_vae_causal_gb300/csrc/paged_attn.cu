@@ -358,7 +358,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant_
             const int rows = meta[stage];
             // S = Q K^T: columns 2 t and 2 t + 1 of each 8 rows of a group, heads g, g + 8
             float sc[NG][2][4] = {};
-if constexpr (Q4) {
+            if constexpr (Q4) {
                 // a piece is 16 or 32 elements, blocks of 16 with an offset each
                 static_assert(S::KC == 1, "one piece of a row for each thread");
                 constexpr int kWords = S::KB / 4;
@@ -402,32 +402,32 @@ if constexpr (Q4) {
                     }
             } else {
 #pragma unroll
-            for (int c = 0; c < S::KC; ++c) {
-                uint4 w4[NG][2];
-#pragma unroll
-                for (int i = 0; i < NG; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        w4[i][j] = *reinterpret_cast<const uint4 *>(
-                            src + i * 2 * S::kHalf + c * 64 / S::SB * 16 * S::SB +
-                            S::piece(8 * j + S::row_of(g), c * 4 % (S::SB / 16) + t));
-                constexpr int kPiece = Q8 ? 4 : 2;  // steps of a piece
-#pragma unroll
-                for (int k = 0; k < kPiece; ++k) {
-                    const int s = c * kPiece + k;
+                for (int c = 0; c < S::KC; ++c) {
+                    uint4 w4[NG][2];
 #pragma unroll
                     for (int i = 0; i < NG; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t w[4] = {w4[i][j].x, w4[i][j].y, w4[i][j].z, w4[i][j].w};
-                            const uint32_t b0 = Q8 ? e4m3x2_to_f16x2(w[k % 4]) : w[(2 * k) % 4];
-                            const uint32_t b1 = Q8 ? e4m3x2_to_f16x2(w[k % 4] >> 16)
-                                                   : w[(2 * k + 1) % 4];
-                            mma_16816<Q8>(sc[i][j], qa[s][0][0], NH > 1 ? qa[s][0][NH - 1] : 0u,
-                                          qa[s][1][0], NH > 1 ? qa[s][1][NH - 1] : 0u, b0, b1);
-                        }
+                        for (int j = 0; j < 2; ++j)
+                            w4[i][j] = *reinterpret_cast<const uint4 *>(
+                                src + i * 2 * S::kHalf + c * 64 / S::SB * 16 * S::SB +
+                                S::piece(8 * j + S::row_of(g), c * 4 % (S::SB / 16) + t));
+                    constexpr int kPiece = Q8 ? 4 : 2;  // steps of a piece
+#pragma unroll
+                    for (int k = 0; k < kPiece; ++k) {
+                        const int s = c * kPiece + k;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t w[4] = {w4[i][j].x, w4[i][j].y, w4[i][j].z, w4[i][j].w};
+                                const uint32_t b0 = Q8 ? e4m3x2_to_f16x2(w[k % 4]) : w[(2 * k) % 4];
+                                const uint32_t b1 = Q8 ? e4m3x2_to_f16x2(w[k % 4] >> 16)
+                                                       : w[(2 * k + 1) % 4];
+                                mma_16816<Q8>(sc[i][j], qa[s][0][0], NH > 1 ? qa[s][0][NH - 1] : 0u,
+                                              qa[s][1][0], NH > 1 ? qa[s][1][NH - 1] : 0u, b0, b1);
+                            }
+                    }
                 }
-            }
             }
             // the rows' scales: keys' as factors, values' as exponents.  Column c of
             // this thread's two is byte t of the 4 rows 4 c .. of 8 (rows of 128 bytes)
@@ -524,9 +524,9 @@ if constexpr (Q4) {
                 // their sums below fp16's products' fp32 range, and O is seldom rescaled
                 if (__any_sync(0xffffffffu, mx > m[h] + kLag || low)) {
                     if (Q8) {
-                        // A value row of zeros (scale 1: e = 0; of 4 bits, the smallest) has no part in the maximum:
-                        // it would take the bits of the weights that count.  The eight
-                        // lanes of a t look at a row together.
+                        // A value row of zeros (scale 1: e = 0; of 4 bits, the smallest) has
+                        // no part in the maximum: it would take the bits of the weights that
+                        // count.  The eight lanes of a t look at a row together.
                         bool unsure = false;
                         if (!Q4)
 #pragma unroll
@@ -901,11 +901,16 @@ int head_block(int G) { return G <= 8 ? 8 : 16; }
 //
 // Rows of 4 bits cost more to look up in registers than there, so it takes them earlier, and of
 // both widths.  8 kv heads, 1 / 4 / 8 query heads a kv head, here then there, rows of 128: one
-// sequence of 300 9.1 9.5 10.1 and 11.1 10.7 11.7, of 2500 14.5 15.0 16.2 and 11.6 12.0 13.0,
-// of 131040 72 72 73 and 46 46 55; 64 of 300 23 23 25 and 25 27 37, of 1000 42 43 45 and 35 36
-// 53, of 2100 86 88 89 and 55 57 82, of 17 to 8192 148 151 155 and 88 90 122; rows of 64: one
-// of 131040 54 54 54 and 36 37 47, 64 of 300 18 18 19 and 22 23 32, of 1000 31 32 32 and 28 29
-// 46, of 2100 65 66 66 and 44 46 67.
+// sequence of 300 9.1 9.5 10.1 and 11.1 10.7 11.7, of 700 12.5 13.0 13.6 and 11.5 11.5 10.9, of
+// 2500 14.5 15.0 16.2 and 11.6 12.0 13.0, of 131040 72 72 73 and 46 46 55; 64 of 300 23 23 25 and
+// 25 27 37, of 700 32.6 33.9 35.5 and 32.6 33.7 47, of 1000 42 43 45 and 35 36 53, of 2100 86 88
+// 89 and 55 57 82, of 17 to 8192 148 151 155 and 88 90 122; rows of 64: one of 131040 54 54 54
+// and 36 37 47, 64 of 300 18 18 19 and 22 23 32, of 700 25.4 25.8 26.5 and 28.8 29.3 41.4, of 980
+// 32.3 32.8 33.4 and 33.2 34.1 47.5, of 2100 65 66 66 and 44 46 67.  So with 64 sequences the
+// two are even at 700 rows of 128 and at 1000 of 64 up to 4 heads, and near 2000 for 8; few sequences
+// would gain there earlier (a single one from 500 rows on, by 1 to 5 us).  What is not known is how
+// long the sequences are: behind a wide table, short ones pay the difference (64 of 300 rows of
+// 8 heads: 25 us here, 37 there).
 bool on_tc(const KvCacheSpec &c, int G, int max_pages, int n_seq) {
     const int64_t rows = (int64_t)max_pages << c.log2_page;
     if (G > 8) return false;

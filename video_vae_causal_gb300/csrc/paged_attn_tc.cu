@@ -49,10 +49,11 @@
 // rate); one of 131040 rows, 8 heads of 8: 50 us (5.4 TB/s, 0.80; about 8 us of it
 // the launches, the first loads' latency and the join).
 //
-// Over 4 bits, instructions: the batch takes 90 us (3.2 TB/s, 0.48), the one sequence 54
-// (2.7 TB/s, 0.40), with 0.56 instructions issued a quarter of an SM and cycle, half of them for
-// the look-up.  Without its arithmetic (timing alone) they take 74 and 44, without the
-// softmax's 89 and 52.
+// Over 4 bits, the look-up's instructions and the chain from one role to the next: the batch takes
+// 90 us (3.2 TB/s, 0.48), the one sequence 55 (2.7 TB/s, 0.40), with 0.56 instructions issued a
+// quarter of an SM and cycle, half of them for the look-up, and the longest waits those for
+// barriers and TMEM.  Without the look-up's arithmetic (timing alone) they take 74 and 44, without
+// the softmax's 89 and 52.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -830,8 +831,10 @@ __device__ __forceinline__ float warp_sums(float (&v)[HP], int lane) {
 }
 
 // The weights of one row of a unit of 4 bits, as P's words, and its part of the sums, and the
-// thread's largest s + e + 7 - m, above 8 where m has to move first; true where r has to.  A weight is rounded to fp16 (2^-11 of itself); from there
-// on two heads take an instruction, and the three e4m3 terms hold its 11 bits.
+// thread's largest s + e + 7 - m, above 8 where m has to move first; true where r has to.  A
+// weight is rounded to fp16 (2^-11 of itself, where the terms of the 8-bit cache's hold 2^-12;
+// an eighth of what the bf16 output rounds by); from there on two heads take an instruction, and the
+// three e4m3 terms hold its 11 bits.
 template <class C>
 __device__ __forceinline__ bool weights4(const uint8_t *smem, const float *own,
                                          const float (&m)[C::HP], float (&l)[C::HP],

@@ -11,8 +11,8 @@
 // Angles.  A position of 10^5 times a frequency near one leaves 32-bit floats seven bits of
 // the turn, fewer than bf16 has.  A frequency is therefore held as a 64-bit fraction of a
 // turn (its whole turns do not matter, positions being whole numbers), and the product with
-// the position, modulo 2^64, is the angle's fraction of a turn, exact to 2^-32 in its upper
-// half: one integer multiplication, no table, any position.
+// the position, modulo 2^64, is the angle's fraction of a turn, its upper half within 2^-31 of a
+// turn: one integer multiplication, no table, any position.
 //
 // A head is D / 8 lanes of four pairs each, so the two elements of a pair are in one
 // thread; a warp holds the same head of 256 / D tokens at a time, each lane with the sines and
@@ -22,14 +22,17 @@
 // two elements an instruction (packed fp32).  Tokens, cut into as many pieces of their heads
 // as it takes to keep the warps busy, go to the warps in turn.
 //
-// Sines and cosines of bf16 rows are the fast ones: over half a turn they are off by less than
-// 2^-21 (absolute), which a bf16 result has no bits for; fp32 rows take the exact ones.
+// Sines and cosines of bf16 rows are the fast ones, off by less than 2^-20 (absolute: the
+// functions' 2^-21.19 over half a turn, and pi 2^-23 of the angle's rounding and its product
+// with pi), 2^-12 of what a result of the pair's size rounds by; fp32 rows take the exact ones,
+// 2^-22 off with the angle's rounding.
 //
 // What bounds it: HBM, behind the chain of a head's sum (four shuffles, a root) with 24 warps a
 // multiprocessor: 16384 tokens of 32 + 8 heads of 128 in bf16 take 68.7 us (4.9 TB/s, 0.72 of
 // the measured copy rate), 131040 of 6 + 6 heads of 64 turned by three positions 76.1 (5.3 TB/s,
-// 0.78).  Heads one by one, a warp holding several of one token: 77 and 100 us; loads through
-// shared memory, eight deep: 82 and 131.
+// 0.78).  The other order of the pairs: 67.5 and 79.7; in fp32 131 and 134 (5.1 and 6.0 TB/s;
+// floors of 99.5 and 119.5).  Heads one by one, a warp holding several of one token: 77 and
+// 100 us; loads through shared memory, eight deep: 82 and 131.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -49,7 +52,9 @@ constexpr int kEach = 4;    // pieces of work for each warp, where there are few
 // Heads of a lane that are loaded together, while those before them are worked on, and
 // resident blocks.  16384 tokens of 32 + 8 heads of 128 and 131040 of 6 + 6 of 64, bf16, in us:
 // 2 heads and 3 blocks 68.7 and 76.1, 3 and 3 73 and 81, 4 and 2 65 and 92, 4 and 3 79 and 88
-// (spills), 6 and 2 69 and 81, 2 and 4 75 and 81.
+// (spills), 6 and 2 69 and 81, 2 and 4 75 and 81.  One pair of numbers for all variants: with 2 and
+// 3 each has 80 registers and spills a little (8 to 28 bytes in bf16, 40 to 80 in fp32), with 4 and
+// 2 those of bf16 spill nothing, which pays for heads of 128 and costs those of 64.
 constexpr int kFlight = 2;
 constexpr int kBlocks = 3;
 
